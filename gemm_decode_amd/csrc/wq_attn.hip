@@ -1,0 +1,532 @@
+// Attention over the 8-bit key/value cache.
+//
+//   out = sum_j softmax_j(scale * q . k_j) v_j,  k_j = qk_j 2^ek,  v_j = qv_j 2^ev,
+//
+// with one pass over the keys (running maximum m, sum l and output O of a row; a new maximum
+// scales l and O by 2^(m - m')).  The query heads that share a key/value head are rows of
+// one tile: row r of a sequence is query token r / G, head r % G, so the codes are read and
+// decoded once for all of them.
+//
+// Both products run on the matrix cores in fp16 on exact operands: codes become q (v_perm_b32
+// puts u = q + 128 under the exponent byte of 1024.0, one packed add of -1152 leaves q), a
+// query row is scaled by a power of two to put its largest element near 2^14 (bf16 elements
+// down to 2^-31 of it are exact in fp16), and the page's 2^ek joins the fp32 score.  The
+// softmax weights are rounded to fp16, the one rounding to fewer bits before the output: a
+// weight is held as 2^14 p, so 38 binades below a row's largest survive (its relative
+// rounding, at most 2^-11, lies below the 2^-8 of a bf16 output), and the page's 2^ev joins
+// it as 2^(ev - evr) relative to the largest exponent seen, evr (O is in units of 2^evr).
+//
+// The scores are computed transposed, S^T = K Q^T, and so is O^T = V^T P^T: the accumulator
+// layout of S^T (a lane holds one row's scores) is, up to an order of the keys that the
+// cache's layout of the values repeats, the operand layout of P^T, so the weights go from
+// product to product in registers.
+//
+// The keys of a row tile are cut into chunks that run as workgroups of their own where the
+// row tiles alone leave CUs idle; a second kernel joins their partial outputs.
+#include <algorithm>
+
+#include "wq_internal.h"
+
+namespace wq {
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;        // waves of a workgroup of the row kernel
+constexpr int kStep = 32;        // keys of one step of a wave
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kWeightBits = 14.f;  // weights are held as 2^14 p
+
+// --- what a row tile of a sequence sees ---
+struct Tile {
+  int64_t row;        // token row of the sequence's first query
+  int32_t rows;       // rows of the sequence (queries x group)
+  int32_t r0, r1;     // the tile's rows r0 .. r1 - 1
+  int32_t pos0;       // position of query 0 (may be negative)
+  int32_t kv;         // keys the sequence holds
+  int32_t lo, hi;     // keys that any of the tile's rows sees: lo .. hi - 1, lo a multiple of 32
+  int32_t splits;     // chunks of that range (at least 1)
+};
+
+__device__ __forceinline__ int32_t last_key(const AttnArgs& a, const Tile& t, int i) {
+  return a.causal ? min(t.pos0 + i, t.kv - 1) : t.kv - 1;
+}
+__device__ __forceinline__ int32_t first_key(const AttnArgs& a, const Tile& t, int i) {
+  return a.window > 0 ? max((int64_t)t.pos0 + i - a.window + 1, (int64_t)0) : 0;
+}
+
+// false: no such rows
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int s, int tile, Tile& t) {
+  int64_t n;
+  if (a.c.offsets) {
+    const int64_t o0 = min(max((int64_t)a.c.offsets[s], (int64_t)0), a.c.tokens);
+    const int64_t o1 = min(max((int64_t)a.c.offsets[s + 1], o0), a.c.tokens);
+    t.row = o0;
+    n = min(o1 - o0, (int64_t)a.c.max_tokens);
+  } else {
+    t.row = (int64_t)s * a.c.max_tokens;
+    n = a.c.max_tokens;
+  }
+  t.rows = (int32_t)n * a.group;
+  t.r0 = tile * a.tile_rows;
+  if (t.r0 >= t.rows) return false;
+  t.r1 = (int32_t)min((int64_t)t.r0 + a.tile_rows, (int64_t)t.rows);
+  const int64_t raw = max(a.kv_lens ? (int64_t)a.kv_lens[s] : max((int64_t)a.c.starts[s], (int64_t)0) + n, (int64_t)0);
+  t.kv = (int32_t)min(raw, (int64_t)a.cap);
+  // (a query position beyond 31 bits sees what the last position does)
+  t.pos0 = (int32_t)min(raw - n, (int64_t)INT32_MAX - n);
+  const int i0 = t.r0 / a.group, i1 = (t.r1 - 1) / a.group;
+  t.hi = last_key(a, t, i1) + 1;
+  t.lo = first_key(a, t, i0) & ~(kStep - 1);
+  if (t.hi <= t.lo) t.hi = t.lo;
+  t.splits = max((int32_t)(((int64_t)t.hi - t.lo + a.chunk - 1) / a.chunk), 1);
+  return true;
+}
+
+// --- number formats ---
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) + __builtin_bit_cast(f16x2_t, b));
+}
+// codes u = q + 128 of bytes 0, 1 (lo) and 2, 3 (hi) of a word -> exact fp16 q pairs
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  return add_f16x2(__builtin_amdgcn_perm(0x64646464u, w, 0x04010400u), 0xE480E480u);
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  return add_f16x2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u), 0xE480E480u);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  f16x2_t v;
+  v.x = (_Float16)lo;
+  v.y = (_Float16)hi;
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                0, 0);
+}
+// 2^(b - 127) of an exponent byte (0: 0, 255: NaN)
+__device__ __forceinline__ float scale_of(int b) { return b == 255 ? __builtin_nanf("") : __uint_as_float((uint32_t)b << 23); }
+__device__ __forceinline__ uint16_t round16(float v, bool f16) {
+  return f16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// all-reduce over the four lanes of a row (l, l ^ 16, l ^ 32, l ^ 48), without LDS
+__device__ __forceinline__ float max_over_groups(float v) {
+  auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_over_groups(float v) {
+  auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Query rows as fp16 operands: lane (r = lane % 16, g = lane / 16) takes row r, columns 64 blk
+// + 16 g + 8 s + j of operand 2 blk + s.  Returns the factor that takes the scaling by a
+// power of two out of the score (times scale * log2 e).
+template <int DB>
+__device__ __forceinline__ float load_query(const AttnArgs& a, const uint16_t* q, bool live, u32x4_t (&op)[2 * DB]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  uint4 raw[2 * DB];
+  float big = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int o = 0; o < 2 * DB; ++o) {
+    const int d = 64 * (o >> 1) + 16 * g + 8 * (o & 1);
+    raw[o] = make_uint4(0, 0, 0, 0);
+    if (live && d < a.c.dim) raw[o] = *(const uint4*)(q + d);
+  }
+  float x[2 * DB][8];
+#pragma unroll
+  for (int o = 0; o < 2 * DB; ++o) {
+    const uint32_t w[4] = {raw[o].x, raw[o].y, raw[o].z, raw[o].w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t h = (w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+      x[o][j] = a.f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)h) : __uint_as_float(h << 16);
+      const float m = __builtin_fabsf(x[o][j]);
+      bad |= !(m < __builtin_inff());
+      big = fmaxf(big, m);
+    }
+  }
+  big = max_over_groups(bad ? __builtin_inff() : big);
+  // 2^(14 - floor(log2 big)), held to normal numbers; the product then lies below 2^15
+  const int E = (int)(__float_as_uint(big) >> 23);
+  const int up = E == 255 ? 127 : min(268 - E, 253);
+  const float mul = __uint_as_float((uint32_t)up << 23), back = __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+  for (int o = 0; o < 2 * DB; ++o)
+    op[o] = u32x4_t{pack_f16x2(x[o][0] * mul, x[o][1] * mul), pack_f16x2(x[o][2] * mul, x[o][3] * mul),
+                    pack_f16x2(x[o][4] * mul, x[o][5] * mul), pack_f16x2(x[o][6] * mul, x[o][7] * mul)};
+  return back * a.scale_log2;
+}
+
+// Where a finished row goes: 8 columns from d on, v already the row's output (or normalised
+// partial output).
+__device__ __forceinline__ void store_out8(const AttnArgs& a, int64_t tok, int qh, int d, const float (&v)[8]) {
+  if (d >= a.c.dim) return;
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = round16(v[2 * j], a.f16) | (uint32_t)round16(v[2 * j + 1], a.f16) << 16;
+  *(uint4*)(a.out.p + tok * a.out.ts + (int64_t)qh * a.out.hs + d) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ------------------------------------------------------------------ the row kernel
+// A workgroup of 4 waves takes 16 NB rows of one key/value head and one chunk of keys; its
+// waves take consecutive quarters of the chunk in steps of 32 keys, codes straight from
+// memory to operands (the cache's layout: every load is one contiguous KB of a wave), the
+// next step's codes in flight while the current one is multiplied.
+template <int DB, int NB>
+__global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
+  constexpr int RS = 132;  // floats of a row of the exchange buffer (128 + 4: no bank conflicts)
+  __shared__ float ex[kWaves * 16 * RS];
+  __shared__ float stat_m[kWaves][16 * NB], stat_l[kWaves][16 * NB];
+  int64_t id = blockIdx.x;
+  const int split = (int)(id % a.splits);
+  id /= a.splits;
+  const int tile = (int)(id % a.tiles);
+  id /= a.tiles;
+  const int hk = (int)(id % a.c.heads);
+  const int s = (int)(id / a.c.heads);
+  Tile t;
+  if (!find_tile(a, s, tile, t) || split >= t.splits) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+
+  u32x4_t q[NB][2 * DB];
+  float cq[NB];
+  int32_t last[NB], first[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = t.r0 + 16 * nb + r;
+    const bool live = row < t.r1;
+    const int i = (live ? row : t.r0) / a.group, qh = hk * a.group + (live ? row : t.r0) % a.group;
+    cq[nb] = load_query<DB>(a, a.q.p + (t.row + i) * a.q.ts + (int64_t)qh * a.q.hs, live, q[nb]);
+    last[nb] = live ? last_key(a, t, i) : -1;
+    first[nb] = live ? first_key(a, t, i) : 0;
+  }
+  // keys that every row of the tile sees need no mask (a dead row's output is not stored)
+  const int32_t all_last = last_key(a, t, t.r0 / a.group), all_first = first_key(a, t, (t.r1 - 1) / a.group);
+
+  const int32_t c0 = t.lo + split * a.chunk, c1 = (int32_t)min((int64_t)c0 + a.chunk, (int64_t)t.hi);
+  const int32_t steps = (c1 - c0 + kStep - 1) / kStep, per = (steps + kWaves - 1) / kWaves;
+  const int32_t w0 = c0 + wave * per * kStep, w1 = c0 + min(steps, (wave + 1) * per) * kStep;
+
+  f32x4_t O[NB][4 * DB];
+  float m[NB], l[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    m[nb] = kNegInf;
+    l[nb] = 0.f;
+#pragma unroll
+    for (int o = 0; o < 4 * DB; ++o) O[nb][o] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  int evr = 0;  // O is in units of 2^(evr - 127)
+
+  const int64_t head_bytes = (int64_t)(64 * DB) << a.c.tshift;
+  const int slot_mask = (1 << a.c.tshift) - 1;
+  for (int32_t base = w0; base < w1; base += 64 * 16) {
+    // the next 64 groups of 16 keys: lane i holds group i's page and exponents
+    const int32_t pos = base + 16 * lane;
+    int page = 0, ek = 0, ev = 0;
+    if (pos < c1) {
+      page = a.c.table[(int64_t)s * a.c.width + (pos >> a.c.tshift)];
+      if ((uint32_t)page < (uint64_t)a.c.pages) {
+        ek = a.c.ke[(int64_t)page * a.c.heads + hk];
+        ev = a.c.ve[(int64_t)page * a.c.heads + hk];
+      } else {
+        page = 0;
+        ek = ev = 255;  // outside the pool: reads as NaN
+      }
+    }
+    uint4 kw[2][2][DB], vw[2][2][DB];  // [buffer][group][block]
+    auto load = [&](int st, int buf) {
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        const int pg = __builtin_amdgcn_readlane(page, 2 * st + gr);
+        const int64_t off = ((int64_t)pg * a.c.heads + hk) * head_bytes +
+                            (int64_t)((base + st * kStep + 16 * gr) & slot_mask) * (64 * DB) + lane * 16;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) {
+          kw[buf][gr][b] = load_stream16(a.c.kc + off + b * 1024);
+          vw[buf][gr][b] = load_stream16(a.c.vc + off + b * 1024);
+        }
+      }
+    };
+    auto compute = [&](int st, int buf) {
+      const int32_t key0 = base + st * kStep;
+      f32x4_t S[NB][2];
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) S[nb][gr] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < DB; ++b) {
+          const uint4 w = kw[buf][gr][b];
+          const u32x4_t k0 = {codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y)};
+          const u32x4_t k1 = {codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w)};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            S[nb][gr] = mma(k0, q[nb][2 * b], S[nb][gr]);
+            S[nb][gr] = mma(k1, q[nb][2 * b + 1], S[nb][gr]);
+          }
+        }
+      }
+      const int ek0 = __builtin_amdgcn_readlane(ek, 2 * st), ek1 = __builtin_amdgcn_readlane(ek, 2 * st + 1);
+      const int ev0 = __builtin_amdgcn_readlane(ev, 2 * st), ev1 = __builtin_amdgcn_readlane(ev, 2 * st + 1);
+      const float kf[2] = {scale_of(ek0), scale_of(ek1)};
+      // the largest value exponent so far (255, NaN, is no exponent)
+      const int e_new = max(evr, max(ev0 == 255 ? 0 : ev0, ev1 == 255 ? 0 : ev1));
+      const int sink = evr - e_new;  // <= 0
+      evr = e_new;
+      const float o_shift = sink <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + sink) << 23);
+      const int d0 = ev0 - evr, d1 = ev1 - evr;
+      const float vf[2] = {ev0 == 255 ? __builtin_nanf("") : d0 <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + d0) << 23),
+                           ev1 == 255 ? __builtin_nanf("") : d1 <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + d1) << 23)};
+      const bool mask = key0 + kStep - 1 > all_last || key0 < all_first;
+      u32x4_t P[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float sc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sc[e] = S[nb][e >> 2][e & 3] * (kf[e >> 2] * cq[nb]);
+        if (mask) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int32_t key = key0 + 16 * (e >> 2) + 4 * g + (e & 3);
+            if (key > last[nb] || key < first[nb]) sc[e] = kNegInf;
+          }
+        }
+        float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+        mx = fmaxf(max_over_groups(mx), m[nb]);
+        if (__builtin_amdgcn_ballot_w64(mx > m[nb]) != 0 || sink != 0) {
+          const float al = mx > m[nb] ? __builtin_amdgcn_exp2f(m[nb] - mx) : 1.f;
+          l[nb] *= al;
+          const float f = al * o_shift;
+#pragma unroll
+          for (int o = 0; o < 4 * DB; ++o) O[nb][o] *= f;
+          m[nb] = mx;
+        }
+        const float ref = (m[nb] == kNegInf ? 0.f : m[nb]) - kWeightBits;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(sc[e] - ref);
+          l[nb] += p[e];
+          if (p[e] > 0.f) p[e] *= vf[e >> 2];  // (a masked weight stays 0 beside a NaN page)
+        }
+        P[nb] = u32x4_t{pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]), pack_f16x2(p[4], p[5]), pack_f16x2(p[6], p[7])};
+      }
+#pragma unroll
+      for (int b = 0; b < DB; ++b) {
+        const uint4 x = vw[buf][0][b], y = vw[buf][1][b];
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const u32x4_t v = {codes_lo(xw[c]), codes_hi(xw[c]), codes_lo(yw[c]), codes_hi(yw[c])};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) O[nb][4 * b + c] = mma(v, P[nb], O[nb][4 * b + c]);
+        }
+      }
+    };
+    const int n = min(32, (w1 - base) / kStep);
+    load(0, 0);
+    for (int st = 0; st < n; st += 2) {
+      if (st + 1 < n) load(st + 1, 1);
+      compute(st, 0);
+      if (st + 1 < n) {
+        if (st + 2 < n) load(st + 2, 0);
+        compute(st + 1, 1);
+      }
+    }
+  }
+
+  // the waves' results meet: common maximum, sum, and each wave's share of the output
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    l[nb] = sum_over_groups(l[nb]);
+    if (g == 0) {
+      stat_m[wave][16 * nb + r] = m[nb];
+      stat_l[wave][16 * nb + r] = l[nb];
+    }
+  }
+  __syncthreads();
+  const bool direct = t.splits == 1;
+  const int64_t all_rows = a.c.tokens * ((int64_t)a.c.heads * a.group);
+  const float unit = scale_of(evr);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float mg = kNegInf, lg = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) mg = fmaxf(mg, stat_m[w][16 * nb + r]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = stat_m[w][16 * nb + r];
+      if (mw > kNegInf || stat_l[w][16 * nb + r] != 0.f) lg += stat_l[w][16 * nb + r] * __builtin_amdgcn_exp2f(mw > kNegInf ? mw - mg : 0.f);
+    }
+    // (first the division, then the unit: the product of the two may leave fp32)
+    const float share = m[nb] > kNegInf ? __builtin_amdgcn_exp2f(m[nb] - mg) / lg : lg != lg ? lg : 0.f;
+    const int row = t.r0 + 16 * nb + r;
+    if (wave == 0 && g == 0 && row < t.r1) {
+      const int i = row / a.group, qh = hk * a.group + row % a.group;
+      const int64_t at = (t.row + i) * ((int64_t)a.c.heads * a.group) + qh;
+      const float lse2 = lg == 0.f ? kNegInf : mg + __builtin_log2f(lg) - kWeightBits;
+      if (!direct) a.part_l[split * all_rows + at] = lse2;
+      else if (a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
+    }
+#pragma unroll
+    for (int b0 = 0; b0 < DB; b0 += 2) {  // 128 columns at a time
+      if (nb > 0 || b0 > 0) __syncthreads();
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (b0 + b < DB) {
+          float* e = ex + (wave * 16 + r) * RS + 64 * b + 16 * g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // columns 16 g + 4 i + c
+            *(float4*)(e + 4 * i) =
+                make_float4(O[nb][4 * (b0 + b)][i] * share * unit, O[nb][4 * (b0 + b) + 1][i] * share * unit,
+                            O[nb][4 * (b0 + b) + 2][i] * share * unit, O[nb][4 * (b0 + b) + 3][i] * share * unit);
+        }
+      __syncthreads();
+      const int orow = threadIdx.x >> 4, oc = (threadIdx.x & 15) * 8, row2 = t.r0 + 16 * nb + orow;
+      if (row2 < t.r1 && 64 * b0 + oc < 64 * DB) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          float4 f = *(const float4*)(ex + orow * RS + oc + j);
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) {
+            const float4 h = *(const float4*)(ex + (w * 16 + orow) * RS + oc + j);
+            f.x += h.x;
+            f.y += h.y;
+            f.z += h.z;
+            f.w += h.w;
+          }
+          v[j] = f.x;
+          v[j + 1] = f.y;
+          v[j + 2] = f.z;
+          v[j + 3] = f.w;
+        }
+        const int i = row2 / a.group, qh = hk * a.group + row2 % a.group;
+        if (direct) {
+          store_out8(a, t.row + i, qh, 64 * b0 + oc, v);
+        } else {
+          const int64_t at = (t.row + i) * ((int64_t)a.c.heads * a.group) + qh;
+          float* po = a.part_o + (split * all_rows + at) * (64 * DB) + 64 * b0 + oc;
+          *(float4*)po = make_float4(v[0], v[1], v[2], v[3]);
+          *(float4*)(po + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- joining the splits
+// One group of 8 x blocks lanes per row: out = sum_s w_s O_s / sum_s w_s, w_s = 2^(lse_s - max).
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  const int per = 8 * a.c.blocks;  // threads of a row (8 columns each)
+  const int64_t id = (int64_t)blockIdx.x * (256 / per) + threadIdx.x / per;
+  const int d = (threadIdx.x % per) * 8;
+  if (threadIdx.x >= 256 / per * per) return;
+  const int64_t max_rows = (int64_t)a.c.max_tokens * a.group;
+  const int64_t rr = id % max_rows;
+  const int hk = (int)((id / max_rows) % a.c.heads);
+  const int64_t s = id / max_rows / a.c.heads;
+  if (s >= a.c.seqs) return;
+  Tile t;
+  if (!find_tile(a, (int)s, (int)(rr / a.tile_rows), t) || rr >= t.rows || t.splits == 1) return;
+  const int i = (int)rr / a.group, qh = hk * a.group + (int)rr % a.group;
+  const int64_t q_heads = (int64_t)a.c.heads * a.group, all_rows = a.c.tokens * q_heads;
+  const int64_t at = (t.row + i) * q_heads + qh;
+  float mx = kNegInf, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < t.splits; ++k) mx = fmaxf(mx, a.part_l[k * all_rows + at]);
+  for (int k = 0; k < t.splits; ++k) {
+    const float lse = a.part_l[k * all_rows + at];
+    if (lse == kNegInf) continue;  // a chunk that this row does not see
+    const float w = __builtin_amdgcn_exp2f(lse - mx);
+    sum += w;
+    const float4* p = (const float4*)(a.part_o + (k * all_rows + at) * (64 * a.c.blocks) + d);
+    const float4 x = p[0], y = p[1];
+    v[0] += w * x.x;
+    v[1] += w * x.y;
+    v[2] += w * x.z;
+    v[3] += w * x.w;
+    v[4] += w * y.x;
+    v[5] += w * y.y;
+    v[6] += w * y.z;
+    v[7] += w * y.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = sum == 0.f ? 0.f : v[j] / sum;
+  store_out8(a, t.row + i, qh, d, v);
+  if (a.lse && d == 0) a.lse[at] = sum == 0.f ? kNegInf : (mx + __builtin_log2f(sum)) * 0.69314718055994530942f;
+}
+
+// NB of the row kernel: the rows of the longest sequence, as far as the registers go
+int row_blocks(const AttnArgs& a) {
+  const int64_t rows = (int64_t)a.c.max_tokens * a.group;
+  const int top = a.c.blocks <= 2 ? 4 : 2;
+  int nb = 1;
+  while (nb < top && 16 * nb < rows) nb *= 2;
+  return nb;
+}
+
+}  // namespace
+
+size_t plan_attention(AttnArgs* a, size_t ws_bytes) {
+  a->tile_rows = 16 * row_blocks(*a);
+  a->tiles = (int32_t)(((int64_t)a->c.max_tokens * a->group + a->tile_rows - 1) / a->tile_rows);
+  // keys a row tile may see, rounded for its start at a multiple of 32
+  const int64_t q_tokens = (a->tile_rows - 1) / a->group + 2;
+  const int64_t seen = a->window > 0 ? std::min<int64_t>(a->cap, (int64_t)a->window + q_tokens) : a->cap;
+  const int64_t span = (seen + 2 * kStep - 1) / kStep * kStep;
+  const int64_t items = (int64_t)a->c.seqs * a->c.heads * a->tiles;
+  const int64_t rows = a->c.tokens * (int64_t)a->c.heads * a->group;
+  const size_t per = (size_t)rows * (64 * a->c.blocks + 1) * sizeof(float);
+  const int64_t unit = kWaves * kStep;
+  int64_t splits = (2048 + items - 1) / items;
+  splits = std::min<int64_t>(splits, (span + unit - 1) / unit);
+  if ((size_t)splits > ws_bytes / per) splits = (int64_t)(ws_bytes / per);
+  if (splits < 2) splits = 1;
+  int64_t chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
+  a->chunk = (int32_t)std::min<int64_t>(chunk, INT32_MAX / 2);
+  a->splits = (int32_t)((span + chunk - 1) / chunk);
+  return a->splits > 1 ? per * a->splits : 0;
+}
+
+wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
+  const __int128 blocks = (__int128)a.c.seqs * a.c.heads * a.tiles * a.splits;
+  if (blocks > INT32_MAX) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
+  const int nb = a.tile_rows / 16;
+  auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, 64 * kWaves, 0, s>>>(a); };
+  switch (a.c.blocks * 8 + nb) {
+    case 1 * 8 + 1: go(attn_rows_kernel<1, 1>); break;
+    case 1 * 8 + 2: go(attn_rows_kernel<1, 2>); break;
+    case 1 * 8 + 4: go(attn_rows_kernel<1, 4>); break;
+    case 2 * 8 + 1: go(attn_rows_kernel<2, 1>); break;
+    case 2 * 8 + 2: go(attn_rows_kernel<2, 2>); break;
+    case 2 * 8 + 4: go(attn_rows_kernel<2, 4>); break;
+    case 3 * 8 + 1: go(attn_rows_kernel<3, 1>); break;
+    case 3 * 8 + 2: go(attn_rows_kernel<3, 2>); break;
+    case 4 * 8 + 1: go(attn_rows_kernel<4, 1>); break;
+    case 4 * 8 + 2: go(attn_rows_kernel<4, 2>); break;
+    default: return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: no kernel for this head_dim");
+  }
+  WQ_HIP_CHECK(hipGetLastError());
+  if (a.splits > 1) {
+    const int64_t rows = (int64_t)a.c.seqs * a.c.heads * a.c.max_tokens * a.group, per = 256 / (8 * a.c.blocks);
+    if ((rows + per - 1) / per > INT32_MAX) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
+    attn_join_kernel<<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a);
+    WQ_HIP_CHECK(hipGetLastError());
+  }
+  return WQ_OK;
+}
+
+}  // namespace wq

@@ -227,6 +227,60 @@ wq_status launch_topk(const uint16_t* logits, int64_t M, int64_t V, int k, float
 wq_status launch_moe(const wq_weight* w, int E, const uint16_t* x, const int32_t* offsets, int64_t T, uint16_t* y,
                      bool gated, size_t qw_stride, size_t sc_stride, size_t zs_stride, hipStream_t s);
 
+// Rotary positions (strides in elements; see wq_rope).
+struct RopeArgs {
+  const uint16_t* x;
+  uint16_t* y;
+  int64_t x_ts, x_hs, y_ts, y_hs, tokens;
+  int32_t heads, dim, half, interleaved, axes, f16;
+  const int32_t* pos;
+  const uint8_t* pair_axis;
+  const float* inv_freq;
+};
+wq_status launch_rope(const RopeArgs& a, hipStream_t s);
+
+// One call on the key/value cache: the cache and the batch as the kernels take them.
+struct KvArgs {
+  uint8_t* kc;
+  uint8_t* vc;
+  uint8_t* ke;
+  uint8_t* ve;
+  const int32_t* table;
+  const int32_t* starts;
+  const int32_t* offsets;
+  int64_t pages, width, tokens;
+  int32_t seqs, heads, dim, blocks;  // blocks: 64-column blocks of a head (D64 / 64)
+  int32_t tshift;                    // log2(page_tokens)
+  int32_t max_tokens;
+};
+struct KvTokens {  // a [tokens][heads][dim] tensor (strides in elements)
+  uint16_t* p;
+  int64_t ts, hs;
+};
+wq_status launch_kv_write(const KvArgs& a, const KvTokens& k, const KvTokens& v, bool f16, hipStream_t s);
+wq_status launch_kv_read(const KvArgs& a, const KvTokens& k, const KvTokens& v, bool f16, hipStream_t s);
+
+struct AttnArgs {
+  KvArgs c;
+  KvTokens q, out;
+  float* lse;
+  const int32_t* kv_lens;
+  int32_t group;      // query heads per key/value head
+  int32_t cap;        // keys at or beyond this position are cut off
+  int32_t causal, window, f16;
+  float scale_log2;   // scale * log2(e)
+  int32_t tile_rows;  // rows (token, query head of one key/value head) of a row tile
+  int32_t tiles;      // row tiles of the longest sequence
+  int32_t chunk;      // keys per split
+  int32_t splits;     // most splits of any row tile
+  float* part_o;      // [splits][tokens * query heads][D64]: normalised partial outputs
+  float* part_l;      // [splits][tokens * query heads]: their log2 sums
+};
+// Fills a's tile_rows, tiles, chunk and splits for the workspace given; returns the bytes of
+// partial results that choice takes.
+size_t plan_attention(AttnArgs* a, size_t ws_bytes);
+wq_status launch_attention(const AttnArgs& a, hipStream_t s);
+
 // Device tag "<arch>:<CUs>" of the current device; empty on failure.
 std::string current_device_tag();
 

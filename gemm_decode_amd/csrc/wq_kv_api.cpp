@@ -1,0 +1,270 @@
+// C ABI entry points of the attention block: rotary positions, the 8-bit key/value cache
+// and attention over it.  Host code only: validation, then one launcher each.
+#include <cmath>
+#include <cstdint>
+#include <string>
+
+#include "wq_internal.h"
+
+namespace wq {
+namespace {
+
+bool bad_align(const void* p, size_t a) { return ((uintptr_t)p % a) != 0; }
+
+// The error texts allocate: no C++ exception may leave a C entry point.
+template <class F>
+wq_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return WQ_ERR_INVALID_ARG;
+  }
+}
+
+constexpr int kKvMaxDim = 256;
+constexpr int64_t kMaxCount = INT32_MAX;
+
+// Elements from the first to one past the last of a [tokens][heads][dim] tensor (strides >= 0;
+// at least 1); false when the count leaves 62 bits.
+bool extent(int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t dim, int64_t* out) {
+  const __int128 e = (__int128)(tokens > 0 ? tokens - 1 : 0) * ts + (__int128)(heads - 1) * hs + dim;
+  if (e <= 0 || e > ((__int128)1 << 61)) return false;
+  *out = (int64_t)e;
+  return true;
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+  return pa < pb + (uintptr_t)nb * 2 && pb < pa + (uintptr_t)na * 2;
+}
+
+wq_status check_cache_shape(int64_t pages, int page_tokens, int heads, int head_dim) {
+  if (pages < 1 || pages > kMaxCount || heads < 1 || head_dim < 1)
+    return fail(WQ_ERR_INVALID_ARG, "kv cache: pages (up to 2^31 - 1), heads and head_dim must be >= 1");
+  if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128)
+    return fail(WQ_ERR_UNSUPPORTED, "kv cache: page_tokens must be 16, 32, 64 or 128");
+  if (head_dim % 8 != 0 || head_dim > kKvMaxDim)
+    return fail(WQ_ERR_UNSUPPORTED, "kv cache: head_dim must be a multiple of 8, at most 256");
+  if (heads > 65536) return fail(WQ_ERR_UNSUPPORTED, "kv cache: at most 65536 heads");
+  if ((__int128)pages * heads * page_tokens * kKvMaxDim >= ((__int128)1 << 62))
+    return fail(WQ_ERR_UNSUPPORTED, "kv cache: pool too large");
+  return WQ_OK;
+}
+
+wq_status kv_args(const wq_kv_cache* c, const wq_kv_batch* b, bool device, KvArgs* a) {
+  if (!c || !b) return fail(WQ_ERR_INVALID_ARG, "NULL cache or batch");
+  wq_status st = check_cache_shape(c->pages, c->page_tokens, c->heads, c->head_dim);
+  if (st != WQ_OK) return st;
+  if (b->seqs < 0 || b->tokens < 0 || b->max_tokens < 0 || b->table_width < 1 || b->seqs > kMaxCount ||
+      b->tokens > kMaxCount || b->max_tokens > kMaxCount || b->table_width > kMaxCount)
+    return fail(WQ_ERR_INVALID_ARG, "kv batch: counts must lie in 0 .. 2^31 - 1, table_width in 1 .. 2^31 - 1");
+  if (device) {
+    if (!c->k_codes || !c->v_codes || !c->k_exps || !c->v_exps)
+      return fail(WQ_ERR_INVALID_ARG, "kv cache: NULL codes or exponents");
+    if (bad_align(c->k_codes, 16) || bad_align(c->v_codes, 16))
+      return fail(WQ_ERR_ALIGNMENT, "kv cache: codes must be 16-byte aligned");
+    if (b->seqs > 0 && (!b->table || !b->starts)) return fail(WQ_ERR_INVALID_ARG, "kv batch: NULL table or starts");
+    if (bad_align(b->table, 4) || bad_align(b->starts, 4) || bad_align(b->offsets, 4))
+      return fail(WQ_ERR_ALIGNMENT, "kv batch: table, starts and offsets must be 4-byte aligned");
+    if (!b->offsets && b->tokens != b->seqs * b->max_tokens)
+      return fail(WQ_ERR_INVALID_ARG, "kv batch: without offsets, tokens must be seqs * max_tokens");
+  }
+  a->kc = (uint8_t*)c->k_codes;
+  a->vc = (uint8_t*)c->v_codes;
+  a->ke = (uint8_t*)c->k_exps;
+  a->ve = (uint8_t*)c->v_exps;
+  a->table = b->table;
+  a->starts = b->starts;
+  a->offsets = b->offsets;
+  a->pages = c->pages;
+  a->width = b->table_width;
+  a->tokens = b->tokens;
+  a->seqs = (int32_t)b->seqs;
+  a->heads = c->heads;
+  a->dim = c->head_dim;
+  a->blocks = (c->head_dim + 63) / 64;
+  a->tshift = __builtin_ctz(c->page_tokens);
+  a->max_tokens = (int32_t)b->max_tokens;
+  return WQ_OK;
+}
+
+wq_status check_tokens(const char* what, const void* p, int64_t ts, int64_t hs, int64_t tokens, int64_t heads,
+                       int64_t dim, int64_t* n) {
+  if (!p) return fail(WQ_ERR_INVALID_ARG, std::string(what) + " must not be NULL");
+  if (ts < 0 || hs < 0) return fail(WQ_ERR_INVALID_ARG, std::string(what) + ": negative stride");
+  if (bad_align(p, 16) || ts % 8 != 0 || hs % 8 != 0)
+    return fail(WQ_ERR_ALIGNMENT, std::string(what) + ": needs 16-byte alignment and strides in multiples of 8");
+  if (!extent(tokens, ts, heads, hs, dim, n)) return fail(WQ_ERR_UNSUPPORTED, std::string(what) + ": strides too large");
+  return WQ_OK;
+}
+
+// Two elements of a tensor that is written may not share a place.
+wq_status check_disjoint_rows(const char* what, int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t dim) {
+  const bool head_inner = heads == 1 || hs >= dim;
+  const bool by_token = tokens <= 1 || ts >= (heads - 1) * hs + dim;                 // [token][head]
+  const bool by_head = heads == 1 || (ts >= dim && hs >= (tokens - 1) * ts + dim);   // [head][token]
+  if (tokens > 0 && !((head_inner && by_token) || (by_head && (tokens <= 1 || ts >= dim))))
+    return fail(WQ_ERR_INVALID_ARG, std::string(what) + ": rows overlap");
+  return WQ_OK;
+}
+
+bool bad_act(int act) { return act != WQ_ACT_BF16 && act != WQ_ACT_F16; }
+
+wq_status kv_copy(bool write, const wq_kv_cache* c, const wq_kv_batch* b, int act, const void* k, int64_t k_ts,
+                  int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs, void* stream) {
+  KvArgs a;
+  wq_status st = kv_args(c, b, true, &a);
+  if (st != WQ_OK) return st;
+  if (bad_act(act)) return fail(WQ_ERR_INVALID_ARG, "unknown activation type");
+  if (a.seqs == 0 || a.tokens == 0 || a.max_tokens == 0) return WQ_OK;
+  int64_t nk = 0, nv = 0;
+  if ((st = check_tokens("k", k, k_ts, k_hs, a.tokens, a.heads, a.dim, &nk)) != WQ_OK) return st;
+  if ((st = check_tokens("v", v, v_ts, v_hs, a.tokens, a.heads, a.dim, &nv)) != WQ_OK) return st;
+  const KvTokens kt{(uint16_t*)k, k_ts, k_hs}, vt{(uint16_t*)v, v_ts, v_hs};
+  if (write) return launch_kv_write(a, kt, vt, act == WQ_ACT_F16, (hipStream_t)stream);
+  if ((st = check_disjoint_rows("k", k_ts, k_hs, a.tokens, a.heads, a.dim)) != WQ_OK) return st;
+  if ((st = check_disjoint_rows("v", v_ts, v_hs, a.tokens, a.heads, a.dim)) != WQ_OK) return st;
+  return launch_kv_read(a, kt, vt, act == WQ_ACT_F16, (hipStream_t)stream);
+}
+
+// The part of an attention call that decides its split.
+wq_status attn_shape(const wq_kv_cache* c, const wq_kv_batch* b, bool device, int q_heads, int64_t max_kv, AttnArgs* a) {
+  wq_status st = kv_args(c, b, device, &a->c);
+  if (st != WQ_OK) return st;
+  if (q_heads < 1 || q_heads % c->heads != 0)
+    return fail(WQ_ERR_INVALID_ARG, "wq_kv_attention: q_heads must be a multiple of the cache's heads");
+  if (q_heads / c->heads > 64)
+    return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: at most 64 query heads per key/value head");
+  if (max_kv < 0) return fail(WQ_ERR_INVALID_ARG, "wq_kv_attention: max_kv must be >= 0");
+  const int64_t room = b->table_width <= (kMaxCount >> a->c.tshift) ? b->table_width << a->c.tshift : kMaxCount;
+  // positions are 32-bit and rounded up to a split's length: the last 2^16 stay free
+  a->cap = (int32_t)(max_kv > 0 && max_kv < room ? max_kv : room);
+  if (a->cap > kMaxCount - (1 << 16))
+    return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: max_kv (or the table) must stay below 2^31 - 2^16 tokens");
+  a->group = q_heads / c->heads;
+  if ((int64_t)b->max_tokens * a->group > kMaxCount || b->tokens * q_heads > kMaxCount)
+    return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: tokens * q_heads must stay below 2^31");
+  return WQ_OK;
+}
+
+}  // namespace
+}  // namespace wq
+
+using namespace wq;
+
+extern "C" {
+
+wq_status wq_rope(int act, const void* x, int64_t x_ts, int64_t x_hs, void* y, int64_t y_ts, int64_t y_hs,
+                  int64_t tokens, int heads, int head_dim, int rot_dim, int interleaved, const int32_t* positions,
+                  int axes, const uint8_t* pair_axis, const float* inv_freq, void* stream) {
+  return guarded([&]() -> wq_status {
+    if (bad_act(act)) return fail(WQ_ERR_INVALID_ARG, "unknown activation type");
+    if (tokens < 0 || tokens > kMaxCount || heads < 1 || axes < 1 || x_ts < 0 || x_hs < 0 || y_ts < 0 || y_hs < 0)
+      return fail(WQ_ERR_INVALID_ARG, "wq_rope: bad token, head or axis count, or a negative stride");
+    if (head_dim < 2 || head_dim > 4096 || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > head_dim)
+      return fail(WQ_ERR_INVALID_ARG, "wq_rope: needs an even rot_dim, 0 < rot_dim <= head_dim <= 4096");
+    if (tokens == 0) return WQ_OK;
+    if (!x || !y || !positions || !inv_freq) return fail(WQ_ERR_INVALID_ARG, "NULL argument");
+    if (bad_align(x, 2) || bad_align(y, 2) || bad_align(positions, 4) || bad_align(inv_freq, 4))
+      return fail(WQ_ERR_ALIGNMENT, "wq_rope: x and y need 2-byte, positions and inv_freq 4-byte alignment");
+    int64_t nx = 0, ny = 0;
+    if (!extent(tokens, x_ts, heads, x_hs, head_dim, &nx) || !extent(tokens, y_ts, heads, y_hs, head_dim, &ny))
+      return fail(WQ_ERR_UNSUPPORTED, "wq_rope: strides too large");
+    const wq_status st = check_disjoint_rows("wq_rope: y", y_ts, y_hs, tokens, heads, head_dim);
+    if (st != WQ_OK) return st;
+    const bool in_place = x == y && (x_ts == y_ts || tokens == 1) && (x_hs == y_hs || heads == 1);
+    if (!in_place && overlap(x, nx, y, ny)) return fail(WQ_ERR_INVALID_ARG, "wq_rope: y overlaps x and is not x itself");
+    RopeArgs a;
+    a.x = (const uint16_t*)x;
+    a.y = (uint16_t*)y;
+    a.x_ts = x_ts;
+    a.x_hs = x_hs;
+    a.y_ts = y_ts;
+    a.y_hs = y_hs;
+    a.tokens = tokens;
+    a.heads = heads;
+    a.dim = in_place ? rot_dim : head_dim;  // in place, what is not turned stays as it is
+    a.half = rot_dim / 2;
+    a.interleaved = interleaved != 0;
+    a.axes = axes;
+    a.f16 = act == WQ_ACT_F16;
+    a.pos = positions;
+    a.pair_axis = pair_axis;
+    a.inv_freq = inv_freq;
+    return launch_rope(a, (hipStream_t)stream);
+  });
+}
+
+wq_status wq_kv_cache_sizes(int64_t pages, int page_tokens, int heads, int head_dim, size_t* code_bytes,
+                            size_t* exp_bytes) {
+  return guarded([&]() -> wq_status {
+    const wq_status st = check_cache_shape(pages, page_tokens, heads, head_dim);
+    if (st != WQ_OK) return st;
+    if (code_bytes) *code_bytes = (size_t)pages * heads * page_tokens * ((head_dim + 63) / 64 * 64);
+    if (exp_bytes) *exp_bytes = (size_t)pages * heads;
+    return WQ_OK;
+  });
+}
+
+wq_status wq_kv_write(const wq_kv_cache* cache, const wq_kv_batch* batch, int act, const void* k, int64_t k_ts,
+                      int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs, void* stream) {
+  return guarded([&] { return kv_copy(true, cache, batch, act, k, k_ts, k_hs, v, v_ts, v_hs, stream); });
+}
+
+wq_status wq_kv_read(const wq_kv_cache* cache, const wq_kv_batch* batch, int act, void* k, int64_t k_ts, int64_t k_hs,
+                     void* v, int64_t v_ts, int64_t v_hs, void* stream) {
+  return guarded([&] { return kv_copy(false, cache, batch, act, k, k_ts, k_hs, v, v_ts, v_hs, stream); });
+}
+
+wq_status wq_kv_attention_workspace_size(const wq_kv_cache* cache, const wq_kv_batch* batch, int q_heads,
+                                         int64_t max_kv, size_t* bytes) {
+  return guarded([&]() -> wq_status {
+    if (!bytes) return fail(WQ_ERR_INVALID_ARG, "NULL argument");
+    AttnArgs a{};
+    const wq_status st = attn_shape(cache, batch, false, q_heads, max_kv, &a);
+    if (st != WQ_OK) return st;
+    *bytes = a.c.seqs == 0 || a.c.tokens == 0 || a.c.max_tokens == 0 ? 0 : plan_attention(&a, SIZE_MAX);
+    return WQ_OK;
+  });
+}
+
+wq_status wq_kv_attention(const wq_kv_cache* cache, const wq_kv_batch* batch, int act, const void* q, int64_t q_ts,
+                          int64_t q_hs, int q_heads, void* out, int64_t o_ts, int64_t o_hs, float* lse,
+                          const int32_t* kv_lens, int64_t max_kv, float scale, int causal, int64_t window, void* ws,
+                          size_t ws_bytes, void* stream) {
+  return guarded([&]() -> wq_status {
+    AttnArgs a{};
+    wq_status st = attn_shape(cache, batch, true, q_heads, max_kv, &a);
+    if (st != WQ_OK) return st;
+    if (bad_act(act)) return fail(WQ_ERR_INVALID_ARG, "unknown activation type");
+    if (!std::isfinite(scale)) return fail(WQ_ERR_INVALID_ARG, "wq_kv_attention: scale must be finite");
+    if (window < 0 || (window > 0 && !causal))
+      return fail(WQ_ERR_INVALID_ARG, "wq_kv_attention: window must be >= 0, and 0 when not causal");
+    if (a.c.seqs == 0 || a.c.tokens == 0 || a.c.max_tokens == 0) return WQ_OK;
+    int64_t nq = 0, no = 0;
+    if ((st = check_tokens("q", q, q_ts, q_hs, a.c.tokens, q_heads, a.c.dim, &nq)) != WQ_OK) return st;
+    if ((st = check_tokens("out", out, o_ts, o_hs, a.c.tokens, q_heads, a.c.dim, &no)) != WQ_OK) return st;
+    if ((st = check_disjoint_rows("out", o_ts, o_hs, a.c.tokens, q_heads, a.c.dim)) != WQ_OK) return st;
+    if (overlap(q, nq, out, no)) return fail(WQ_ERR_INVALID_ARG, "wq_kv_attention: out overlaps q");
+    if (bad_align(lse, 4) || bad_align(kv_lens, 4))
+      return fail(WQ_ERR_ALIGNMENT, "wq_kv_attention: lse and kv_lens must be 4-byte aligned");
+    if (ws && bad_align(ws, 256)) return fail(WQ_ERR_ALIGNMENT, "wq_kv_attention: the workspace must be 256-byte aligned");
+    a.q = KvTokens{(uint16_t*)q, q_ts, q_hs};
+    a.out = KvTokens{(uint16_t*)out, o_ts, o_hs};
+    a.lse = lse;
+    a.kv_lens = kv_lens;
+    a.causal = causal != 0;
+    a.window = window >= INT32_MAX ? 0 : (int32_t)window;
+    a.f16 = act == WQ_ACT_F16;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    plan_attention(&a, ws ? ws_bytes : 0);
+    if (a.splits > 1) {
+      const int64_t rows = a.c.tokens * q_heads;
+      a.part_o = (float*)ws;
+      a.part_l = a.part_o + (int64_t)a.splits * rows * a.c.blocks * 64;
+    }
+    return launch_attention(a, (hipStream_t)stream);
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,128 @@
+// Rotary positions over one or several axes.
+//
+// Pair i of a head turns by positions[axis(i)][t] * inv_freq[i].  The angle is formed in
+// turns in 64 bits, t = pos * inv_freq / (2 pi), and only its fractional part goes on in
+// fp32 (an fp32 product of a position near 10^5 would already be off by 2^-8 of a radian);
+// the hardware sine and cosine take turns, so no further reduction follows.
+//
+// A thread takes 8 pairs of one token and walks a share of the heads: the angles of a token
+// are the same for every head, so sine and cosine are paid once per share, and a head's 8
+// pairs are two 16-byte loads and stores (one 32-byte run when interleaved).  What lies
+// behind the turned elements is copied by further threads of the same kind.
+#include "wq_internal.h"
+
+namespace wq {
+namespace {
+
+struct __attribute__((packed, aligned(2))) Vec8 {  // 8 elements at any element's alignment
+  uint32_t w[4];
+};
+
+template <bool F16>
+__device__ __forceinline__ float to_f32(uint32_t b) {
+  return F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)b) : __uint_as_float(b << 16);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t from_f32(float v) {
+  return F16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+template <bool F16>
+__device__ __forceinline__ void turn(float c, float s, uint32_t& a, uint32_t& b) {
+  const float x1 = to_f32<F16>(a), x2 = to_f32<F16>(b);
+  a = from_f32<F16>(x1 * c - x2 * s);
+  b = from_f32<F16>(x2 * c + x1 * s);
+}
+
+// one thread: chunk `c` of one token, heads h0, h0 + step, ...
+template <bool F16, bool INTER>
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int turn_chunks, int chunks, int shares) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int c = (int)(id % chunks);
+  const int64_t r = id / chunks;
+  const int share = (int)(r % shares);
+  const int64_t t = r / shares;
+  if (t >= a.tokens) return;
+  const uint16_t* x = a.x + t * a.x_ts;
+  uint16_t* y = a.y + t * a.y_ts;
+  if (c >= turn_chunks) {  // behind the turned elements
+    const int d0 = 2 * a.half + 8 * (c - turn_chunks), n = min(8, a.dim - d0);
+    for (int h = share; h < a.heads; h += shares) {
+      const uint16_t* xs = x + h * a.x_hs + d0;
+      uint16_t* ys = y + h * a.y_hs + d0;
+      if (n == 8) *(Vec8*)ys = *(const Vec8*)xs;
+      else
+        for (int j = 0; j < n; ++j) ys[j] = xs[j];
+    }
+    return;
+  }
+  const int i0 = 8 * c, n = min(8, a.half - i0);
+  float cs[8], sn[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = min(i0 + j, a.half - 1);
+    const int ax = a.pair_axis ? min((int)a.pair_axis[i], a.axes - 1) : 0;
+    const double tr = (double)a.pos[(int64_t)ax * a.tokens + t] * ((double)a.inv_freq[i] * 0.15915494309189533577);
+    const float f = (float)(tr - __builtin_rint(tr));
+    cs[j] = __builtin_amdgcn_cosf(f);
+    sn[j] = __builtin_amdgcn_sinf(f);
+  }
+  if (n == 8) {
+    const int d1 = INTER ? 2 * i0 : i0, d2 = INTER ? 2 * i0 + 8 : i0 + a.half;
+    for (int h = share; h < a.heads; h += shares) {
+      const uint16_t* xs = x + h * a.x_hs;
+      uint16_t* ys = y + h * a.y_hs;
+      Vec8 u = *(const Vec8*)(xs + d1), v = *(const Vec8*)(xs + d2);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (INTER) {  // pair j: the two halves of word j
+          uint32_t& w = j < 4 ? u.w[j] : v.w[j - 4];
+          uint32_t p = w & 0xFFFFu, q = w >> 16;
+          turn<F16>(cs[j], sn[j], p, q);
+          w = p | (q << 16);
+        } else {
+          const int sh = 16 * (j & 1);
+          uint32_t p = (u.w[j >> 1] >> sh) & 0xFFFFu, q = (v.w[j >> 1] >> sh) & 0xFFFFu;
+          turn<F16>(cs[j], sn[j], p, q);
+          u.w[j >> 1] = sh ? (u.w[j >> 1] & 0xFFFFu) | (p << 16) : (u.w[j >> 1] & 0xFFFF0000u) | p;
+          v.w[j >> 1] = sh ? (v.w[j >> 1] & 0xFFFFu) | (q << 16) : (v.w[j >> 1] & 0xFFFF0000u) | q;
+        }
+      }
+      *(Vec8*)(ys + d1) = u;
+      *(Vec8*)(ys + d2) = v;
+    }
+  } else {
+    for (int h = share; h < a.heads; h += shares) {
+      const uint16_t* xs = x + h * a.x_hs;
+      uint16_t* ys = y + h * a.y_hs;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) {
+          const int d1 = INTER ? 2 * (i0 + j) : i0 + j, d2 = INTER ? d1 + 1 : d1 + a.half;
+          uint32_t p = xs[d1], q = xs[d2];
+          turn<F16>(cs[j], sn[j], p, q);
+          ys[d1] = (uint16_t)p;
+          ys[d2] = (uint16_t)q;
+        }
+    }
+  }
+}
+
+}  // namespace
+
+wq_status launch_rope(const RopeArgs& a, hipStream_t s) {
+  const int turn_chunks = (a.half + 7) / 8, chunks = turn_chunks + (a.dim - 2 * a.half + 7) / 8;
+  // shares of the heads: enough threads for 16 waves per CU, at most one head per thread
+  const int64_t base = a.tokens * chunks, want = (int64_t)256 * 16 * 64;
+  int64_t shares = (want + base - 1) / base;
+  if (shares > a.heads) shares = a.heads;
+  const int64_t blocks = (base * shares + 255) / 256;
+  if (blocks > INT32_MAX) return fail(WQ_ERR_UNSUPPORTED, "wq_rope: too many elements for one call");
+  auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, 256, 0, s>>>(a, turn_chunks, chunks, (int)shares); };
+  if (a.f16) a.interleaved ? go(rope_kernel<true, true>) : go(rope_kernel<true, false>);
+  else a.interleaved ? go(rope_kernel<false, true>) : go(rope_kernel<false, false>);
+  WQ_HIP_CHECK(hipGetLastError());
+  return WQ_OK;
+}
+
+}  // namespace wq

@@ -25,6 +25,8 @@ __all__ = [
     "wq_moe_linear", "quantize_experts", "EPILOGUE_NONE", "EPILOGUE_SILU_MUL",
     "ACT", "wq_linear_act", "wq_gemv_act", "wq_gemm_act", "wq_linear_residual", "wq_gemv_residual",
     "wq_gemm_residual",
+    "wq_rope", "KVCache", "KVBatch", "wq_kv_cache_sizes", "wq_kv_write", "wq_kv_read",
+    "wq_kv_attention_workspace_size", "wq_kv_attention",
     "wq_tune_pick", "wq_tune", "wq_tune_cache_set", "wq_tune_cache_get", "wq_tune_cache_clear",
     "wq_tune_cache_save", "wq_tune_cache_load", "quantize", "workspace",
 ]
@@ -62,8 +64,20 @@ class WqWeightC(C.Structure):
                 ("qweight", C.c_void_p), ("scales", C.c_void_p), ("zeros", C.c_void_p)]
 
 
+class WqKvCacheC(C.Structure):
+    _fields_ = [("pages", C.c_int64), ("page_tokens", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32),
+                ("reserved", C.c_int32), ("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_exps", C.c_void_p),
+                ("v_exps", C.c_void_p)]
+
+
+class WqKvBatchC(C.Structure):
+    _fields_ = [("seqs", C.c_int64), ("tokens", C.c_int64), ("max_tokens", C.c_int64), ("table_width", C.c_int64),
+                ("table", C.c_void_p), ("starts", C.c_void_p), ("offsets", C.c_void_p)]
+
+
 _P = C.POINTER
 _W = _P(WqWeightC)
+_KC, _KB = _P(WqKvCacheC), _P(WqKvBatchC)
 _SIGS = {
     "wq_abi_version": (C.c_int, []),
     "wq_status_string": (C.c_char_p, [C.c_int]),
@@ -100,6 +114,18 @@ _SIGS = {
                                  C.c_void_p]),
     "wq_lm_head_topk": (C.c_int, [_W, C.c_void_p, C.c_int64, C.c_int, C.c_float, C.c_void_p, C.c_void_p,
                                   C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "wq_rope": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                          C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p,
+                          C.c_void_p]),
+    "wq_kv_cache_sizes": (C.c_int, [C.c_int64, C.c_int, C.c_int, C.c_int, _P(C.c_size_t), _P(C.c_size_t)]),
+    "wq_kv_write": (C.c_int, [_KC, _KB, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int64,
+                              C.c_void_p]),
+    "wq_kv_read": (C.c_int, [_KC, _KB, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int64,
+                             C.c_void_p]),
+    "wq_kv_attention_workspace_size": (C.c_int, [_KC, _KB, C.c_int, C.c_int64, _P(C.c_size_t)]),
+    "wq_kv_attention": (C.c_int, [_KC, _KB, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int, C.c_void_p, C.c_int64,
+                                  C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_float, C.c_int, C.c_int64,
+                                  C.c_void_p, C.c_size_t, C.c_void_p]),
     "wq_tune_pick": (C.c_int, [_P(C.c_double), C.c_int]),
     "wq_tune": (C.c_int, [_W, C.c_int, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
                           C.c_int, C.c_int, C.c_void_p, _P(C.c_int), _P(C.c_double)]),
@@ -420,6 +446,138 @@ def wq_linear_perm(w: PackedWeight, x: torch.Tensor, perm: torch.Tensor, y: torc
     d = w.desc()
     _check(lib.wq_linear_perm(C.byref(d), _ptr(x), _ptr(perm), M, _ptr(y), _ptr(ws),
                               0 if ws is None else ws.numel(), _stream(stream)), "wq_linear_perm")
+
+
+# ------------------------------------------------- rotary positions, 8-bit key/value cache
+def _same_device(*tensors) -> None:
+    dev = tensors[0].device
+    assert dev.type == "cuda" and all(t is None or t.device == dev for t in tensors), "tensors on different devices"
+
+
+def _heads3(t: torch.Tensor, what: str, dim: int | None = None):
+    """(pointer, token stride, head stride) of a [tokens][heads][dim] tensor."""
+    assert t.dim() == 3 and (dim is None or t.shape[2] == dim), f"{what} must be [tokens][heads][head_dim]"
+    ts, hs, ds = t.stride()
+    assert ds == 1 or t.shape[2] == 1, f"{what}: a head's elements must be contiguous"
+    return t.data_ptr(), ts, hs
+
+
+def _act_of(t: torch.Tensor) -> int:
+    assert t.dtype in (torch.bfloat16, torch.float16), "bf16 or fp16"
+    return _act(t)
+
+
+def wq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+            axis: torch.Tensor | None = None, interleaved: bool = False, stream=None) -> None:
+    """x, y bf16 or fp16 [tokens][heads][dim] (any strides; y may be x); positions int32
+    [axes][tokens] or [tokens]; inv_freq fp32 [rot_dim / 2]; axis uint8 [rot_dim / 2]."""
+    _same_device(x, y, positions, inv_freq, axis)
+    act = _act_of(x)
+    assert y.dtype == x.dtype and y.shape == x.shape
+    tokens, heads, dim = x.shape
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    assert positions.dtype == torch.int32 and positions.is_contiguous() and positions.numel() == axes * tokens
+    assert inv_freq.dtype == torch.float32 and inv_freq.is_contiguous()
+    half = inv_freq.numel()
+    assert axis is None or (axis.dtype == torch.uint8 and axis.is_contiguous() and axis.numel() == half)
+    xp, xt, xh = _heads3(x, "x")
+    yp, yt, yh = _heads3(y, "y")
+    _check(lib.wq_rope(act, xp, xt, xh, yp, yt, yh, tokens, heads, dim, 2 * half, int(interleaved),
+                       positions.data_ptr(), axes, _ptr(axis), inv_freq.data_ptr(), _stream(stream)), "wq_rope")
+
+
+def wq_kv_cache_sizes(pages: int, page_tokens: int, heads: int, head_dim: int):
+    """(bytes of the key codes, bytes of the key exponents); the values' are the same."""
+    c, e = C.c_size_t(), C.c_size_t()
+    _check(lib.wq_kv_cache_sizes(pages, page_tokens, heads, head_dim, C.byref(c), C.byref(e)), "wq_kv_cache_sizes")
+    return c.value, e.value
+
+
+class KVCache:
+    """A pool of pages of 8-bit keys and values (wq_kv_cache); owns its four uint8 tensors,
+    which need no initialisation."""
+
+    def __init__(self, pages: int, page_tokens: int, heads: int, head_dim: int, device="cuda"):
+        self.pages, self.page_tokens, self.heads, self.head_dim = pages, page_tokens, heads, head_dim
+        cb, eb = wq_kv_cache_sizes(pages, page_tokens, heads, head_dim)
+        self.k_codes, self.v_codes = (torch.empty(cb, dtype=torch.uint8, device=device) for _ in range(2))
+        self.k_exps, self.v_exps = (torch.empty(eb, dtype=torch.uint8, device=device) for _ in range(2))
+
+    def desc(self) -> WqKvCacheC:
+        return WqKvCacheC(self.pages, self.page_tokens, self.heads, self.head_dim, 0, self.k_codes.data_ptr(),
+                          self.v_codes.data_ptr(), self.k_exps.data_ptr(), self.v_exps.data_ptr())
+
+    def nbytes(self) -> int:
+        return 2 * (self.k_codes.numel() + self.k_exps.numel())
+
+
+class KVBatch:
+    """The tokens of one step by sequence (wq_kv_batch): table int32 [seqs][pages], starts
+    int32 [seqs], offsets int32 [seqs + 1] (None: max_tokens rows for every sequence),
+    max_tokens the most rows of any sequence.  The tensors are kept, not copied, so a
+    step's program may update them in place."""
+
+    def __init__(self, table: torch.Tensor, starts: torch.Tensor, offsets: torch.Tensor | None = None,
+                 max_tokens: int = 1):
+        assert table.dtype == torch.int32 and table.dim() == 2 and table.stride(1) == 1
+        seqs = table.shape[0]
+        assert starts.dtype == torch.int32 and starts.is_contiguous() and starts.numel() == seqs
+        assert offsets is None or (offsets.dtype == torch.int32 and offsets.is_contiguous()
+                                   and offsets.numel() == seqs + 1)
+        assert table.is_contiguous(), "the page table must be contiguous"
+        self.table, self.starts, self.offsets, self.max_tokens = table, starts, offsets, max_tokens
+        self.seqs = seqs
+
+    def desc(self, tokens: int) -> WqKvBatchC:
+        return WqKvBatchC(self.seqs, tokens, self.max_tokens, self.table.shape[1], self.table.data_ptr(),
+                          self.starts.data_ptr(), 0 if self.offsets is None else self.offsets.data_ptr())
+
+
+def _kv_copy(f, where, cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream) -> None:
+    _same_device(cache.k_codes, batch.table, k, v)
+    act = _act_of(k)
+    assert v.dtype == k.dtype and v.shape == k.shape and k.shape[1] == cache.heads
+    kp, kt, kh = _heads3(k, "k", cache.head_dim)
+    vp, vt, vh = _heads3(v, "v", cache.head_dim)
+    _check(f(C.byref(cache.desc()), C.byref(batch.desc(k.shape[0])), act, kp, kt, kh, vp, vt, vh, _stream(stream)),
+           where)
+
+
+def wq_kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """Quantise k, v (bf16 or fp16 [tokens][heads][head_dim]) into the cache."""
+    _kv_copy(lib.wq_kv_write, "wq_kv_write", cache, batch, k, v, stream)
+
+
+def wq_kv_read(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """Read the batch's positions back into k, v (bf16 or fp16 [tokens][heads][head_dim])."""
+    _kv_copy(lib.wq_kv_read, "wq_kv_read", cache, batch, k, v, stream)
+
+
+def wq_kv_attention_workspace_size(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int, max_kv: int = 0) -> int:
+    n = C.c_size_t()
+    _check(lib.wq_kv_attention_workspace_size(C.byref(cache.desc()), C.byref(batch.desc(tokens)), q_heads, max_kv,
+                                              C.byref(n)), "wq_kv_attention_workspace_size")
+    return n.value
+
+
+def wq_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, scale: float,
+                    causal: bool = True, window: int = 0, kv_lens: torch.Tensor | None = None, max_kv: int = 0,
+                    lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> None:
+    """q, out bf16 or fp16 [tokens][q_heads][head_dim]; kv_lens int32 [seqs]; lse fp32
+    [tokens][q_heads]; ws a workspace of wq_kv_attention_workspace_size bytes (or less, or None:
+    the keys are then split less)."""
+    _same_device(cache.k_codes, batch.table, q, out, kv_lens, lse, ws)
+    act = _act_of(q)
+    assert out.dtype == q.dtype and out.shape == q.shape
+    assert kv_lens is None or (kv_lens.dtype == torch.int32 and kv_lens.is_contiguous()
+                               and kv_lens.numel() == batch.seqs)
+    assert lse is None or (lse.dtype == torch.float32 and lse.is_contiguous()
+                           and lse.numel() == q.shape[0] * q.shape[1])
+    qp, qt, qh = _heads3(q, "q", cache.head_dim)
+    op, ot, oh = _heads3(out, "out", cache.head_dim)
+    _check(lib.wq_kv_attention(C.byref(cache.desc()), C.byref(batch.desc(q.shape[0])), act, qp, qt, qh, q.shape[1],
+                               op, ot, oh, _ptr(lse), _ptr(kv_lens), max_kv, scale, int(causal), window, _ptr(ws),
+                               0 if ws is None else ws.numel(), _stream(stream)), "wq_kv_attention")
 
 
 # ---------------------------------------------------------------------- tuner

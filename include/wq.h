@@ -472,6 +472,140 @@ wq_status wq_linear_perm_workspace_size(const wq_weight* w, int64_t M, size_t* b
 wq_status wq_linear_perm(const wq_weight* w, const void* x, const int32_t* perm, int64_t M, void* y,
                          void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------- rotary positions */
+
+/* Rotary positions on the heads of x [tokens][heads][head_dim] (bf16, or fp16 with
+ * WQ_ACT_F16; any token and head strides, counted in elements, the head's elements
+ * contiguous; 2-byte aligned) into y (the same type, its own strides).  The pair i < rot_dim
+ * / 2 of every head turns by the angle positions[axis][t] * inv_freq[i], axis =
+ * pair_axis[i] (NULL: axis 0 for every pair):
+ *   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin,
+ * with (x1, x2) = (x[i], x[i + rot_dim / 2]), or (x[2i], x[2i + 1]) when interleaved is not
+ * 0; elements from rot_dim on are copied.  One axis is a text position; three are the time,
+ * height and width of images and video, every pair taking its own axis.  The query and key
+ * heads of one fused QKV row are one call (heads = the two counts together).
+ *
+ * positions: int32 [axes][tokens]; pair_axis: uint8 [rot_dim / 2], values < axes (others
+ * count as axes - 1); inv_freq: fp32 [rot_dim / 2], radians per position (all on the
+ * device).  The angle is reduced to one turn in 64 bits, so a position of any size keeps
+ * its phase; sine, cosine and the products are fp32, rounded once.  rot_dim is even, 0 <
+ * rot_dim <= head_dim <= 4096; axes >= 1.  y may be x itself (same pointer and strides); any other
+ * overlap is WQ_ERR_INVALID_ARG.  Allocates nothing, graph-capturable. */
+wq_status wq_rope(int act, const void* x, int64_t x_token_stride, int64_t x_head_stride, void* y,
+                  int64_t y_token_stride, int64_t y_head_stride, int64_t tokens, int heads, int head_dim,
+                  int rot_dim, int interleaved, const int32_t* positions, int axes, const uint8_t* pair_axis,
+                  const float* inv_freq, void* stream);
+
+/* ------------------------------------------- the 8-bit key/value cache */
+
+/* A pool of pages of page_tokens tokens (16, 32, 64 or 128) for heads key/value heads of
+ * head_dim elements (a multiple of 8, at most 256).  Per page and head the keys and the
+ * values each have one exponent byte b (0 < b < 255) and int8 codes q, |q| <= 127, that
+ * stand for q * 2^(b - 127).
+ *
+ * Power-of-two scales: with e = b - 127 the smallest integer >= -126 such that max|x| <= 127
+ * * 2^e over the tokens a page has taken, q = rint(x / 2^e) (ties to even) is computed
+ * without a rounding of its own, the values are exact in bf16, and when a later token
+ * enlarges a page's scale its older codes only drop low bits (q' = rint(q / 2^d)): however
+ * often that happens the dropped parts add up to less than one step of the final scale,
+ * where a scale of max / 127 would round again at every change.  A NaN or an infinity sets b = 255: the page's values of that head read
+ * as NaN, and every query that sees one of its tokens gives NaN.
+ *
+ * Memory: k_codes and v_codes hold wq_kv_cache_sizes' code bytes each (16-byte aligned),
+ * k_exps and v_exps its exponent bytes ([pages][heads], any alignment).  None needs
+ * initialising.  With D64 = head_dim rounded up to a multiple of 64 (columns from head_dim
+ * on are zero), page p of head h starts at byte (p * heads + h) * page_tokens * D64 and
+ * holds groups of 16 tokens, 16 * D64 bytes each, of 1 KB blocks of 64 columns; a byte is
+ * q + 128.  Byte 16 l + j of a block is
+ *   keys:    token l % 16,                 column 16 (l / 16) + j,
+ *   values:  token 4 (l / 16) + j % 4,     column 4 (l % 16) + j / 4,
+ * the order in which lane l of a wave feeds v_mfma: every wave load is one contiguous KB
+ * and no value crosses lanes. */
+typedef struct {
+  int64_t pages;
+  int32_t page_tokens;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t reserved; /* 0 */
+  void* k_codes;
+  void* v_codes;
+  void* k_exps;
+  void* v_exps;
+} wq_kv_cache;
+
+/* The tokens of one call, grouped by sequence.  Sequence s owns rows offsets[s] ..
+ * offsets[s + 1] - 1 of the token tensors (offsets int32 [seqs + 1], NULL: max_tokens rows
+ * each, tokens = seqs * max_tokens), which are its positions starts[s], starts[s] + 1, ...;
+ * position p lies in pool page table[s * table_width + p / page_tokens].  table, starts and
+ * offsets are on the device.  tokens: rows of the token tensors; max_tokens: the most rows
+ * any sequence has (a longer one is cut there).  Offsets are clamped into [0, tokens];
+ * negative starts count as 0; positions beyond the table are cut off; a page number outside the pool is not
+ * written and reads as NaN.  seqs and tokens may be 0. */
+typedef struct {
+  int64_t seqs;
+  int64_t tokens;
+  int64_t max_tokens;
+  int64_t table_width;
+  const int32_t* table;
+  const int32_t* starts;
+  const int32_t* offsets;
+} wq_kv_batch;
+
+/* Bytes of k_codes (= v_codes) and of k_exps (= v_exps); host only. */
+wq_status wq_kv_cache_sizes(int64_t pages, int page_tokens, int heads, int head_dim, size_t* code_bytes,
+                            size_t* exp_bytes);
+
+/* Quantise the batch's keys and values into the cache: k, v [tokens][heads][head_dim] (bf16,
+ * or fp16 with WQ_ACT_F16; strides in elements and multiples of 8, 16-byte aligned).  A
+ * write that starts inside a page keeps the page's earlier tokens (their codes drop bits
+ * where the scale grows) and a write from a page's first slot on starts it anew; slots
+ * behind the written range hold nothing afterwards.  No two sequences of one call may write
+ * the same page (sharing pages that are only read is fine).  Allocates nothing,
+ * graph-capturable, bit-identical from run to run. */
+wq_status wq_kv_write(const wq_kv_cache* cache, const wq_kv_batch* batch, int act, const void* k,
+                      int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                      int64_t v_head_stride, void* stream);
+
+/* Read the batch's positions back: k, v [tokens][heads][head_dim] in the given type (the
+ * values q * 2^e, exact in bf16 and rounded once in fp16; a value beyond the type's largest
+ * finite one becomes that one; NaN for pages of exponent 255).  Alignment as for wq_kv_write; rows outside every
+ * sequence's range, and rows whose position lies beyond the table, are not written. */
+wq_status wq_kv_read(const wq_kv_cache* cache, const wq_kv_batch* batch, int act, void* k,
+                     int64_t k_token_stride, int64_t k_head_stride, void* v, int64_t v_token_stride,
+                     int64_t v_head_stride, void* stream);
+
+/* Attention of the batch's queries over the cache: out[t][h] = sum_j softmax_j(scale *
+ * q[t][h] . k_j) v_j, key/value head h * heads / q_heads (q_heads a multiple of the cache's
+ * heads, at most 64 queries per key/value head).
+ * q, out [tokens][q_heads][head_dim] in bf16 or fp16 (strides in elements and multiples of
+ * 8, 16-byte aligned; out must not overlap q).  One entry point serves prompts, chunks
+ * behind a cached prefix, drafted tokens and single ones.
+ *
+ * A sequence of n rows sees kv = kv_lens[s] cached tokens (device int32 [seqs]; NULL:
+ * starts[s] + n, the rows' own tokens written before the call).  Row i stands at position p
+ * = kv - n + i.  causal != 0: it sees the keys j <= p, and with window > 0 only those with
+ * j > p - window; causal 0: all kv keys (window must be 0).  A row that sees no key gives
+ * 0 (lse -infinity).  lse: NULL, or fp32 [tokens][q_heads], the natural logarithm of the
+ * row's sum of exp(scale * q . k).  Keys outside a row's view never reach it, whatever
+ * their bytes.
+ *
+ * max_kv: an upper bound of every kv (0: the table's); keys beyond it are cut off, and the
+ * work is split by it.  Scores, statistics and sums are fp32; the softmax weights enter the
+ * second product as fp16 (scaled so that 38 binades below the row's largest survive), the
+ * codes as exact fp16 values.
+ *
+ * ws: room for the partial results of a split over the keys; wq_kv_attention_workspace_size
+ * gives what the best split takes, less (or NULL) only splits less.  Results are
+ * bit-identical from run to run for a given workspace size and device.  Allocates nothing,
+ * graph-capturable. */
+wq_status wq_kv_attention_workspace_size(const wq_kv_cache* cache, const wq_kv_batch* batch, int q_heads,
+                                         int64_t max_kv, size_t* bytes);
+wq_status wq_kv_attention(const wq_kv_cache* cache, const wq_kv_batch* batch, int act, const void* q,
+                          int64_t q_token_stride, int64_t q_head_stride, int q_heads, void* out,
+                          int64_t out_token_stride, int64_t out_head_stride, float* lse, const int32_t* kv_lens,
+                          int64_t max_kv, float scale, int causal, int64_t window, void* ws, size_t ws_bytes,
+                          void* stream);
+
 /* ------------------------------------------------------------------ tuner */
 
 /* Choose among measured candidates: the smallest latency wins and a tie goes to

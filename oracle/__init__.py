@@ -21,6 +21,8 @@ What it computes (plain, slow, obviously correct; NumPy only):
 * ``moe``    -- the grouped (mixture-of-experts) layer, each expert applied to its
   own rows, and the SiLU-gated product of a fused gate/up projection (reading in
   its docstring).
+* ``attention`` -- rotary positions over several axes, the paged 8-bit key/value cache
+  with one power-of-two scale per page and head, and attention over it.
 
 Passages followed:
 
@@ -50,3 +52,4 @@ from .topk import ref_topk_sample, sample_row, topk_row  # noqa: F401
 from .moe import (  # noqa: F401
     check_offsets, ref_linear_silu_mul, ref_moe_linear, ref_moe_silu_mul, silu, silu_mul,
 )
+from .attention import PagedCache, attend, page_exponent, rope  # noqa: F401
