@@ -127,6 +127,21 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+__device__ __forceinline__ float in_f32(uint32_t bits, bool f16) {
+  return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : __uint_as_float(bits << 16);
+}
+// *mul: the power of two that puts a row of largest magnitude `big` below 2^15 (with the sign
+// of the softmax scale, so that what is returned is not negative): 2^(14 - floor(log2 big)),
+// held to normal numbers.  Returns what takes it out of the score, times |scale| log2 e; NaN
+// for a row that is not finite (every score of it is then infinite or NaN, and so is the row).
+__device__ __forceinline__ float query_scale(const AttnArgs& a, float big, float* mul) {
+  const int E = (int)(__float_as_uint(big) >> 23);
+  const int up = E == 255 ? 127 : min(268 - E, 253);
+  const float f = __uint_as_float((uint32_t)up << 23);
+  *mul = a.scale_log2 < 0.f ? -f : f;
+  return E == 255 ? __builtin_nanf("") : __uint_as_float((uint32_t)(254 - up) << 23) * __builtin_fabsf(a.scale_log2);
+}
+
 // Query rows as fp16 operands: lane (r = lane % 16, g = lane / 16) takes row r, columns 64 blk
 // + 16 g + 8 s + j of operand 2 blk + s.  Returns the factor that takes the scaling by a
 // power of two out of the score (times scale * log2 e).
@@ -149,22 +164,19 @@ __device__ __forceinline__ float load_query(const AttnArgs& a, const uint16_t* q
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t h = (w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-      x[o][j] = a.f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)h) : __uint_as_float(h << 16);
+      x[o][j] = in_f32(h, a.f16);
       const float m = __builtin_fabsf(x[o][j]);
       bad |= !(m < __builtin_inff());
       big = fmaxf(big, m);
     }
   }
-  big = max_over_groups(bad ? __builtin_inff() : big);
-  // 2^(14 - floor(log2 big)), held to normal numbers; the product then lies below 2^15
-  const int E = (int)(__float_as_uint(big) >> 23);
-  const int up = E == 255 ? 127 : min(268 - E, 253);
-  const float mul = __uint_as_float((uint32_t)up << 23), back = __uint_as_float((uint32_t)(254 - up) << 23);
+  float mul;
+  const float back = query_scale(a, max_over_groups(bad ? __builtin_inff() : big), &mul);
 #pragma unroll
   for (int o = 0; o < 2 * DB; ++o)
     op[o] = u32x4_t{pack_f16x2(x[o][0] * mul, x[o][1] * mul), pack_f16x2(x[o][2] * mul, x[o][3] * mul),
                     pack_f16x2(x[o][4] * mul, x[o][5] * mul), pack_f16x2(x[o][6] * mul, x[o][7] * mul)};
-  return back * a.scale_log2;
+  return back;
 }
 
 // Where a finished row goes: 8 columns from d on, v already the row's output (or normalised
@@ -428,6 +440,391 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
   }
 }
 
+// ----------------------------------------------------------------- the tile kernel
+// Many rows per key/value head (prompts): a workgroup of W waves takes 32 RB W rows and walks
+// the keys in tiles of KT.  The waves decode a tile's codes together into fp16 operands in
+// LDS, once for all rows and one tile ahead (two buffers, the codes of the tile after that
+// in flight in registers), so decoding costs a row little; every wave then multiplies its own
+// 32 RB rows by the whole tile on v_mfma_f32_32x32x16_f16.
+//
+// LDS holds operands in lane order, 1 KB blocks of 16 bytes per lane: a read is one ds_read_b128
+// over contiguous KB, without bank conflicts.  Keys: block (32 keys, 16 columns), lane (r, h)
+// = key r, columns 8 h + j.  Values: block (16 keys, 32 columns); an accumulator lane (r, h) of
+// S^T holds row r's scores of the keys 8 a + 4 h + b, so slot j of lane half h is key 4 h + j
+// % 4 + 8 (j / 4); operand row 8 m + c is column 4 c + m, the order in which the cache's
+// words come, and the accumulator of O^T then holds 16 consecutive columns per lane.
+//
+// The pages' scales are folded into the decoded operands, q 2^(e - e') relative to the
+// tile's largest key exponent and the largest value exponent so far: one packed fma in the
+// place of the packed add, exact down to 2^-24.
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16_t mma32(u32x4_t a, u32x4_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                0, 0);
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, f16x2_t m, f16x2_t c) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, a), m, c));
+}
+// q 2^d of four codes: lo and hi pair
+struct Decode {
+  f16x2_t mul, sub;  // 2^d, -1152 2^d
+  __device__ __forceinline__ Decode(int e, int ref) {  // e, ref: exponent bytes; e 255: NaN
+    const float f = e == 255 ? __builtin_nanf("") : e - ref < -24 ? 0.f : __uint_as_float((uint32_t)(127 + e - ref) << 23);
+    mul = f16x2_t{(_Float16)f, (_Float16)f};
+    sub = mul * f16x2_t{(_Float16)-1152.f, (_Float16)-1152.f};
+  }
+  __device__ __forceinline__ uint2 operator()(uint32_t w) const {
+    return make_uint2(fma_f16x2(__builtin_amdgcn_perm(0x64646464u, w, 0x04010400u), mul, sub),
+                      fma_f16x2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u), mul, sub));
+  }
+};
+__device__ __forceinline__ int largest_exponent(uint32_t bytes) {  // of four bytes, 255 (NaN) apart
+  int e = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = (bytes >> (8 * i)) & 0xFF;
+    e = max(e, b == 255 ? 0 : b);
+  }
+  return e;
+}
+__device__ __forceinline__ float max_over_halves(float v) {
+  auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float sum_over_halves(float v) {
+  auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+template <int DB, int RB, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnArgs a, int64_t items) {
+  constexpr int KT = 64;                 // keys of a tile: 4 groups of 16
+  constexpr int KS = 4 * DB;             // 16-column steps of a row
+  constexpr int WIN = 64;                // tiles whose pages and exponents are held in LDS
+  constexpr int TH = 64 * W;
+  constexpr int KB = KT * 64 * DB * 2;   // bytes of a tile's keys (or values) as fp16
+  constexpr int CK = KT * 4 * DB, CV = CK / 2;  // 16-byte chunks of a tile's keys, pairs of its values
+  constexpr int NK = (CK + TH - 1) / TH, NV = (CV + TH - 1) / TH;  // of a thread
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * KB];
+  __shared__ int32_t win_page[4 * WIN];
+  __shared__ __attribute__((aligned(16))) uint8_t win_ek[4 * WIN], win_ev[4 * WIN];
+
+  // workgroups go round robin over the 8 XCDs: an XCD takes consecutive items, so the row
+  // tiles of one key/value head share its L2
+  const int64_t per_xcd = (items + 7) / 8;
+  int64_t id = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if (id >= items || (int64_t)(blockIdx.x >> 3) >= per_xcd) return;
+  const int tile = a.tiles - 1 - (int)(id % a.tiles);  // the rows that see most come first
+  id /= a.tiles;
+  const int split = (int)(id % a.splits);
+  id /= a.splits;
+  const int hk = (int)(id % a.c.heads);
+  const int s = (int)(id / a.c.heads);
+  Tile t;
+  if (!find_tile(a, s, tile, t) || split >= t.splits) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, h = lane >> 5;
+
+  // ---- this wave's rows
+  const int wr0 = t.r0 + 32 * RB * wave, wr1 = min(wr0 + 32 * RB, t.r1);
+  u32x4_t q[RB][KS];
+  float cq[RB];
+  int32_t last[RB], first[RB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int row = wr0 + 32 * rb + r;
+    const bool live = row < t.r1;
+    const int i = (live ? row : t.r0) / a.group, qh = hk * a.group + (live ? row : t.r0) % a.group;
+    const uint16_t* src = a.q.p + (t.row + i) * a.q.ts + (int64_t)qh * a.q.hs;
+    uint4 raw[KS];
+    float big = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int d = 16 * k + 8 * h;
+      raw[k] = make_uint4(0, 0, 0, 0);
+      if (live && d < a.c.dim) raw[k] = *(const uint4*)(src + d);
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x0 = __builtin_fabsf(in_f32(w[j] & 0xFFFFu, a.f16)), x1 = __builtin_fabsf(in_f32(w[j] >> 16, a.f16));
+        bad |= !(x0 < __builtin_inff()) || !(x1 < __builtin_inff());
+        big = fmaxf(big, fmaxf(x0, x1));
+      }
+    }
+    float mul;
+    cq[rb] = query_scale(a, max_over_halves(bad ? __builtin_inff() : big), &mul);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q[rb][k][j] = pack_f16x2(in_f32(w[j] & 0xFFFFu, a.f16) * mul, in_f32(w[j] >> 16, a.f16) * mul);
+    }
+    last[rb] = live ? last_key(a, t, i) : -1;
+    first[rb] = live ? first_key(a, t, i) : 0;
+  }
+  // keys that some row, and that every row, of this wave sees
+  const bool any_row = wr0 < t.r1;
+  const int i_lo = (any_row ? wr0 : t.r0) / a.group, i_hi = any_row ? (wr1 - 1) / a.group : i_lo;
+  const int32_t some_last = any_row ? last_key(a, t, i_hi) : -1, some_first = first_key(a, t, i_lo);
+  const int32_t all_last = last_key(a, t, i_lo), all_first = first_key(a, t, i_hi);
+
+  const int32_t c0 = t.lo + split * a.chunk, c1 = (int32_t)min((int64_t)c0 + a.chunk, (int64_t)t.hi);
+  const int32_t tiles = (c1 - c0 + KT - 1) / KT;
+
+  // ---- codes of a tile: memory -> registers -> fp16 operands in LDS
+  const int64_t head_bytes = (int64_t)(64 * DB) << a.c.tshift;
+  const int slot_mask = (1 << a.c.tshift) - 1;
+  uint4 kc[NK], vc[NV][2];
+  uint32_t ek4 = 0, ev4 = 0;  // exponents of the tile held in registers
+  auto fill_window = [&](int j0) {  // tiles j0 .. j0 + WIN - 1
+    for (int i = tid; i < 4 * WIN; i += TH) {
+      const int64_t pos = (int64_t)c0 + (int64_t)j0 * KT + 16 * i;
+      int page = 0, ek = 0, ev = 0;
+      if (pos < c1) {
+        page = a.c.table[(int64_t)s * a.c.width + (pos >> a.c.tshift)];
+        if ((uint32_t)page < (uint64_t)a.c.pages) {
+          ek = a.c.ke[(int64_t)page * a.c.heads + hk];
+          ev = a.c.ve[(int64_t)page * a.c.heads + hk];
+        } else {
+          page = 0;
+          ek = ev = 255;  // outside the pool: reads as NaN
+        }
+      }
+      win_page[i] = page;
+      win_ek[i] = (uint8_t)ek;
+      win_ev[i] = (uint8_t)ev;
+    }
+  };
+  auto load_codes = [&](int j) {
+    const int w0 = 4 * (j % WIN);
+    const int32_t key0 = c0 + j * KT;
+    ek4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ek[w0]);
+    ev4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ev[w0]);
+    // key chunks in the order [group][block][lane], value pairs [group][block][g % 2][column]
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int ch = tid + TH * i, gr = ch / (64 * DB);
+      if (CK % TH != 0 && ch >= CK) break;
+      const int64_t off = ((int64_t)win_page[w0 + gr] * a.c.heads + hk) * head_bytes +
+                          (int64_t)((key0 + 16 * gr) & slot_mask) * (64 * DB) + (ch % (64 * DB)) * 16;
+      kc[i] = *(const uint4*)(a.c.kc + off);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int pr = tid + TH * i, gr = pr / (32 * DB), in = pr % (32 * DB);
+      if (CV % TH != 0 && pr >= CV) break;
+      const int64_t off = ((int64_t)win_page[w0 + gr] * a.c.heads + hk) * head_bytes +
+                          (int64_t)((key0 + 16 * gr) & slot_mask) * (64 * DB) + (in / 32) * 1024 + (in % 32) * 16;
+      vc[i][0] = *(const uint4*)(a.c.vc + off);
+      vc[i][1] = *(const uint4*)(a.c.vc + off + 512);
+    }
+  };
+  int ek_tile = 0, evr = 0;  // reference exponents of the tile last decoded
+  bool v_bad = false;        // it holds a poisoned value page
+  uint32_t v_bytes = 0;
+  auto decode = [&](int buf) {
+    ek_tile = largest_exponent(ek4);
+    evr = max(evr, largest_exponent(ev4));
+    v_bytes = ev4;
+    v_bad = false;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) v_bad |= ((ev4 >> (8 * g)) & 0xFF) == 0xFF;
+    uint8_t* kd = lds[buf];
+    uint8_t* vd = lds[buf] + KB;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int ch = tid + TH * i, gr = ch / (64 * DB), in = ch % (64 * DB);
+      if (CK % TH != 0 && ch >= CK) break;
+      const int ks = 4 * (in / 64) + (in % 64) / 16, key = 16 * gr + in % 16;
+      const Decode dec((ek4 >> (8 * gr)) & 0xFF, ek_tile);
+      const uint2 x = dec(kc[i].x), y = dec(kc[i].y), z = dec(kc[i].z), w = dec(kc[i].w);
+      uint8_t* d = kd + ((key / 32) * KS + ks) * 1024 + (key % 32) * 16;
+      *(uint4*)d = make_uint4(x.x, x.y, y.x, y.y);
+      *(uint4*)(d + 512) = make_uint4(z.x, z.y, w.x, w.y);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int pr = tid + TH * i, gr = pr / (32 * DB), in = pr % (32 * DB);
+      if (CV % TH != 0 && pr >= CV) break;
+      const int e = (ev4 >> (8 * gr)) & 0xFF, g = (in % 32) / 16, c = in % 16;
+      const Decode dec(e == 255 ? 0 : e, evr);  // (a poisoned page is told to the rows that see it)
+      uint8_t* d = vd + (gr * 2 * DB + 2 * (in / 32) + c / 8) * 1024 + g * 512 + (c % 8) * 16;
+      const uint32_t lo[4] = {vc[i][0].x, vc[i][0].y, vc[i][0].z, vc[i][0].w};
+      const uint32_t hi[4] = {vc[i][1].x, vc[i][1].y, vc[i][1].z, vc[i][1].w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint2 x = dec(lo[m]), y = dec(hi[m]);
+        *(uint4*)(d + m * 128) = make_uint4(x.x, x.y, y.x, y.y);
+      }
+    }
+  };
+
+  f32x16_t O[RB][2 * DB];
+  float m[RB], l[RB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    m[rb] = kNegInf;
+    l[rb] = 0.f;
+#pragma unroll
+    for (int o = 0; o < 2 * DB; ++o)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) O[rb][o][e] = 0.f;
+  }
+  int evo = 0;  // O is in units of 2^(evo - 127)
+
+  if (tiles > 0) {
+    fill_window(0);
+    __syncthreads();
+    load_codes(0);
+    decode(0);
+    if (tiles > 1) load_codes(1);
+    __syncthreads();
+  }
+  for (int j = 0; j < tiles; ++j) {
+    const int32_t key0 = c0 + j * KT;
+    const int ekt = ek_tile, evt = evr;
+    const bool poisoned = v_bad;
+    const uint32_t ev_bytes = v_bytes;
+    if (key0 <= some_last && key0 + KT > some_first) {
+      const uint8_t* kd = lds[j & 1] + lane * 16;
+      const uint8_t* vd = kd + KB;
+      f32x16_t S[RB][2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[rb][mt][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const u32x4_t kf = *(const u32x4_t*)(kd + (mt * KS + k) * 1024);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) S[rb][mt] = mma32(kf, q[rb][k], S[rb][mt]);
+        }
+      }
+      const bool mask = key0 + KT - 1 > all_last || key0 < all_first;
+      const int sink = evo - evt;  // <= 0
+      evo = evt;
+      const float o_shift = sink <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + sink) << 23);
+      u32x4_t P[RB][4];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        // (held above 0: a masked -infinity stays one)
+        const float c0 = scale_of(ekt) * cq[rb], tiny = __uint_as_float(1u << 23), c = c0 < tiny ? tiny : c0;
+        if (mask) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int32_t key = key0 + 32 * mt + 8 * (e >> 2) + 4 * h + (e & 3);
+              if (key > last[rb] || key < first[rb]) S[rb][mt][e] = kNegInf;
+            }
+        }
+        float mx = kNegInf;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fmaxf(S[rb][0][e], S[rb][1][e]));
+        mx = fmaxf(max_over_halves(mx) * c, m[rb]);
+        if (__builtin_amdgcn_ballot_w64(mx > m[rb]) != 0 || sink != 0) {
+          const float al = mx > m[rb] ? __builtin_amdgcn_exp2f(m[rb] - mx) : 1.f;
+          l[rb] *= al;
+          const float f = al * o_shift;
+#pragma unroll
+          for (int o = 0; o < 2 * DB; ++o)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) O[rb][o][e] *= f;
+          m[rb] = mx;
+        }
+        const float bias = kWeightBits - (m[rb] == kNegInf ? 0.f : m[rb]);
+        float sum = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            S[rb][mt][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[rb][mt][e], c, bias));
+            sum += S[rb][mt][e];
+          }
+        l[rb] += sum;
+        if (poisoned) {  // a row that sees a key of a poisoned value page is NaN
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int32_t key = key0 + 32 * mt + 8 * (e >> 2) + 4 * h + (e & 3);
+              if (((ev_bytes >> (8 * (2 * mt + (e >> 3)))) & 0xFF) == 0xFF && key <= last[rb] && key >= first[rb])
+                l[rb] = __builtin_nanf("");
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int j2 = 0; j2 < 4; ++j2)
+            P[rb][g][j2] = pack_f16x2(S[rb][g >> 1][8 * (g & 1) + 2 * j2], S[rb][g >> 1][8 * (g & 1) + 2 * j2 + 1]);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int o = 0; o < 2 * DB; ++o) {
+          const u32x4_t vf = *(const u32x4_t*)(vd + (g * 2 * DB + o) * 1024);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) O[rb][o] = mma32(vf, P[rb][g], O[rb][o]);
+        }
+    }
+    if (j + 1 < tiles) {
+      decode((j + 1) & 1);
+      if (j + 2 < tiles) {
+        if ((j + 2) % WIN == 0) {
+          __syncthreads();
+          fill_window(j + 2);
+          __syncthreads();
+        }
+        load_codes(j + 2);
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- outputs: 16 consecutive columns per lane and 32-column block
+  const bool direct = t.splits == 1;
+  const int64_t q_heads = (int64_t)a.c.heads * a.group, all_rows = a.c.tokens * q_heads;
+  const float unit = scale_of(evo);
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const float lg = sum_over_halves(l[rb]);
+    const float share = lg == 0.f ? 0.f : 1.f / lg;
+    const int row = wr0 + 32 * rb + r;
+    if (row >= t.r1) continue;
+    const int i = row / a.group, qh = hk * a.group + row % a.group;
+    const int64_t at = (t.row + i) * q_heads + qh;
+    if (h == 0) {
+      const float lse2 = lg == 0.f ? kNegInf : m[rb] + __builtin_log2f(lg) - kWeightBits;
+      if (!direct) a.part_l[split * all_rows + at] = lse2;
+      else if (a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
+    }
+#pragma unroll
+    for (int o = 0; o < 2 * DB; ++o) {
+      const int d = 32 * o + 16 * h;  // element 4 a + b of the accumulator is column d + 4 b + a
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[4 * (e & 3) + (e >> 2)] = O[rb][o][e] * share * unit;
+      if (direct) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float x[8] = {v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3],
+                              v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
+          store_out8(a, t.row + i, qh, d + 8 * k, x);
+        }
+      } else {
+        float* po = a.part_o + (split * all_rows + at) * (64 * DB) + d;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *(float4*)(po + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- joining the splits
 // One group of 8 x blocks lanes per row: out = sum_s w_s O_s / sum_s w_s, w_s = 2^(lse_s - max).
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
@@ -478,11 +875,18 @@ int row_blocks(const AttnArgs& a) {
   return nb;
 }
 
+// More rows than this take the tile kernel.
+constexpr int kRowKernelRows = 64;
+constexpr int kTileWaves = 8;
+int tile_row_blocks(const AttnArgs&) { return 1; }
+
 }  // namespace
 
 size_t plan_attention(AttnArgs* a, size_t ws_bytes) {
-  a->tile_rows = 16 * row_blocks(*a);
-  a->tiles = (int32_t)(((int64_t)a->c.max_tokens * a->group + a->tile_rows - 1) / a->tile_rows);
+  const int64_t all = (int64_t)a->c.max_tokens * a->group;
+  const bool tiled = all > kRowKernelRows;
+  a->tile_rows = tiled ? 32 * tile_row_blocks(*a) * kTileWaves : 16 * row_blocks(*a);
+  a->tiles = (int32_t)((all + a->tile_rows - 1) / a->tile_rows);
   // keys a row tile may see, rounded for its start at a multiple of 32
   const int64_t q_tokens = (a->tile_rows - 1) / a->group + 2;
   const int64_t seen = a->window > 0 ? std::min<int64_t>(a->cap, (int64_t)a->window + q_tokens) : a->cap;
@@ -490,8 +894,8 @@ size_t plan_attention(AttnArgs* a, size_t ws_bytes) {
   const int64_t items = (int64_t)a->c.seqs * a->c.heads * a->tiles;
   const int64_t rows = a->c.tokens * (int64_t)a->c.heads * a->group;
   const size_t per = (size_t)rows * (64 * a->c.blocks + 1) * sizeof(float);
-  const int64_t unit = kWaves * kStep;
-  int64_t splits = (2048 + items - 1) / items;
+  const int64_t unit = tiled ? 512 : kWaves * kStep;
+  int64_t splits = ((tiled ? 256 : 2048) + items - 1) / items;
   splits = std::min<int64_t>(splits, (span + unit - 1) / unit);
   if ((size_t)splits > ws_bytes / per) splits = (int64_t)(ws_bytes / per);
   if (splits < 2) splits = 1;
@@ -502,22 +906,34 @@ size_t plan_attention(AttnArgs* a, size_t ws_bytes) {
 }
 
 wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
-  const __int128 blocks = (__int128)a.c.seqs * a.c.heads * a.tiles * a.splits;
-  if (blocks > INT32_MAX) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
-  const int nb = a.tile_rows / 16;
-  auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, 64 * kWaves, 0, s>>>(a); };
-  switch (a.c.blocks * 8 + nb) {
-    case 1 * 8 + 1: go(attn_rows_kernel<1, 1>); break;
-    case 1 * 8 + 2: go(attn_rows_kernel<1, 2>); break;
-    case 1 * 8 + 4: go(attn_rows_kernel<1, 4>); break;
-    case 2 * 8 + 1: go(attn_rows_kernel<2, 1>); break;
-    case 2 * 8 + 2: go(attn_rows_kernel<2, 2>); break;
-    case 2 * 8 + 4: go(attn_rows_kernel<2, 4>); break;
-    case 3 * 8 + 1: go(attn_rows_kernel<3, 1>); break;
-    case 3 * 8 + 2: go(attn_rows_kernel<3, 2>); break;
-    case 4 * 8 + 1: go(attn_rows_kernel<4, 1>); break;
-    case 4 * 8 + 2: go(attn_rows_kernel<4, 2>); break;
-    default: return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: no kernel for this head_dim");
+  const __int128 items = (__int128)a.c.seqs * a.c.heads * a.tiles * a.splits;
+  if (items > INT32_MAX - 8) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
+  if ((int64_t)a.c.max_tokens * a.group > kRowKernelRows) {
+    const unsigned blocks = (unsigned)((items + 7) / 8 * 8);
+    auto go = [&](auto kernel) { kernel<<<blocks, 64 * kTileWaves, 0, s>>>(a, (int64_t)items); };
+    switch (a.c.blocks) {
+      case 1: go(attn_tile_kernel<1, 1, kTileWaves>); break;
+      case 2: go(attn_tile_kernel<2, 1, kTileWaves>); break;
+      case 3: go(attn_tile_kernel<3, 1, kTileWaves>); break;
+      case 4: go(attn_tile_kernel<4, 1, kTileWaves>); break;
+      default: return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: no kernel for this head_dim");
+    }
+  } else {
+    const int nb = a.tile_rows / 16;
+    auto go = [&](auto kernel) { kernel<<<(unsigned)items, 64 * kWaves, 0, s>>>(a); };
+    switch (a.c.blocks * 8 + nb) {
+      case 1 * 8 + 1: go(attn_rows_kernel<1, 1>); break;
+      case 1 * 8 + 2: go(attn_rows_kernel<1, 2>); break;
+      case 1 * 8 + 4: go(attn_rows_kernel<1, 4>); break;
+      case 2 * 8 + 1: go(attn_rows_kernel<2, 1>); break;
+      case 2 * 8 + 2: go(attn_rows_kernel<2, 2>); break;
+      case 2 * 8 + 4: go(attn_rows_kernel<2, 4>); break;
+      case 3 * 8 + 1: go(attn_rows_kernel<3, 1>); break;
+      case 3 * 8 + 2: go(attn_rows_kernel<3, 2>); break;
+      case 4 * 8 + 1: go(attn_rows_kernel<4, 1>); break;
+      case 4 * 8 + 2: go(attn_rows_kernel<4, 2>); break;
+      default: return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: no kernel for this head_dim");
+    }
   }
   WQ_HIP_CHECK(hipGetLastError());
   if (a.splits > 1) {
