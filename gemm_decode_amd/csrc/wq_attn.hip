@@ -21,8 +21,8 @@
 // cache's layout of the values repeats, the operand layout of P^T, so the weights go from
 // product to product in registers.
 //
-// The keys of a row tile are cut into chunks that run as workgroups of their own where the
-// row tiles alone leave CUs idle; a second kernel joins their partial outputs.
+// Where the row tiles alone leave CUs idle or unevenly busy, their keys are split and a second
+// kernel joins the partial outputs (normalised, with their log2 sums).
 #include <algorithm>
 
 #include "wq_internal.h"
@@ -48,7 +48,6 @@ struct Tile {
   int32_t pos0;       // position of query 0 (may be negative)
   int32_t kv;         // keys the sequence holds
   int32_t lo, hi;     // keys that any of the tile's rows sees: lo .. hi - 1, lo a multiple of 32
-  int32_t splits;     // chunks of that range (at least 1)
 };
 
 __device__ __forceinline__ int32_t last_key(const AttnArgs& a, const Tile& t, int i) {
@@ -82,8 +81,55 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int s, int tile, Ti
   t.hi = last_key(a, t, i1) + 1;
   t.lo = first_key(a, t, i0) & ~(kStep - 1);
   if (t.hi <= t.lo) t.hi = t.lo;
-  t.splits = max((int32_t)(((int64_t)t.hi - t.lo + a.chunk - 1) / a.chunk), 1);
   return true;
+}
+// chunks of the tile kernel, and steps of the row kernel, of a row tile's keys (at least 1)
+__device__ __forceinline__ int32_t chunks_of(const AttnArgs& a, const Tile& t) {
+  return max((int32_t)(((int64_t)t.hi - t.lo + a.chunk - 1) / a.chunk), 1);
+}
+__device__ __forceinline__ int32_t steps_of(const Tile& t) { return max((t.hi - t.lo + kStep - 1) / kStep, 1); }
+
+// --- equal shares of the row kernel ---
+// The items (sequence and row tile, key/value head) lie one after another on a line, in that
+// order: an item is kItemCost units for what it costs whatever its length (queries, joining
+// the waves), then its steps of 32 keys.  Workgroup w of `shares` takes units w * share ..
+// of the line, whatever items they belong to, so sequences of any lengths load the CUs
+// alike.  Every workgroup forms the line itself (a scan over the sequences' lengths, in
+// LDS); workgroup 0 leaves it in memory for the join.  A workgroup cuts at most two items:
+// the one it starts inside of (its partial results go to slot 2 w) and the one it leaves
+// unfinished (slot 2 w + 1).  Line positions stay below 2^31 (plan_attention sees to it).
+constexpr int kLineMax = 1024;  // sequences x row tiles that the scan takes
+constexpr int kMinShare = 4;    // steps: one per wave
+constexpr int kItemCost = 8;
+
+// line[i]: units of one head before sequence and tile i, 0 <= i <= seqs x tiles; 256 threads
+__device__ __forceinline__ void scan_line(const AttnArgs& a, int32_t* line) {
+  __shared__ int32_t wave_sum[4];
+  const int n = a.c.seqs * a.tiles, per = (n + 255) / 256, tid = threadIdx.x;
+  int32_t sum = 0;
+  for (int i = tid * per; i < min(n, (tid + 1) * per); ++i) {
+    Tile t;
+    const int s = a.tiles == 1 ? i : i / a.tiles;
+    sum += find_tile(a, s, i - s * a.tiles, t) ? steps_of(t) + kItemCost : 0;
+    line[i + 1] = sum;
+  }
+  int32_t incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t o = __shfl_up(incl, d);
+    if ((tid & 63) >= d) incl += o;
+  }
+  if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
+  if (tid == 0) line[0] = 0;
+  __syncthreads();
+  int32_t before = incl - sum;
+  for (int w = 0; w < (tid >> 6); ++w) before += wave_sum[w];
+  for (int i = tid * per; i < min(n, (tid + 1) * per); ++i) line[i + 1] += before;
+  __syncthreads();
+}
+// units of a workgroup's share
+__device__ __forceinline__ int32_t share_of(const AttnArgs& a, int32_t total) {
+  return max((int32_t)(((uint32_t)total + a.shares - 1) / (uint32_t)a.shares), kMinShare);
 }
 
 // --- number formats ---
@@ -142,40 +188,31 @@ __device__ __forceinline__ float query_scale(const AttnArgs& a, float big, float
   return E == 255 ? __builtin_nanf("") : __uint_as_float((uint32_t)(254 - up) << 23) * __builtin_fabsf(a.scale_log2);
 }
 
-// Query rows as fp16 operands: lane (r = lane % 16, g = lane / 16) takes row r, columns 64 blk
-// + 16 g + 8 s + j of operand 2 blk + s.  Returns the factor that takes the scaling by a
-// power of two out of the score (times scale * log2 e).
+// Query rows as fp16 operands: lane (r = lane % 16, g = lane / 16) holds row r, columns 64 b
+// + 16 g + 8 s + j in raw[2 b + s].  Returns query_scale's factor.
 template <int DB>
-__device__ __forceinline__ float load_query(const AttnArgs& a, const uint16_t* q, bool live, u32x4_t (&op)[2 * DB]) {
-  const int g = (threadIdx.x & 63) >> 4;
-  uint4 raw[2 * DB];
+__device__ __forceinline__ float query_operands(const AttnArgs& a, const uint4 (&raw)[2 * DB], u32x4_t (&op)[2 * DB]) {
   float big = 0.f;
   bool bad = false;
 #pragma unroll
   for (int o = 0; o < 2 * DB; ++o) {
-    const int d = 64 * (o >> 1) + 16 * g + 8 * (o & 1);
-    raw[o] = make_uint4(0, 0, 0, 0);
-    if (live && d < a.c.dim) raw[o] = *(const uint4*)(q + d);
-  }
-  float x[2 * DB][8];
-#pragma unroll
-  for (int o = 0; o < 2 * DB; ++o) {
     const uint32_t w[4] = {raw[o].x, raw[o].y, raw[o].z, raw[o].w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t h = (w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-      x[o][j] = in_f32(h, a.f16);
-      const float m = __builtin_fabsf(x[o][j]);
-      bad |= !(m < __builtin_inff());
-      big = fmaxf(big, m);
+    for (int j = 0; j < 4; ++j) {
+      const float x0 = __builtin_fabsf(in_f32(w[j] & 0xFFFFu, a.f16)), x1 = __builtin_fabsf(in_f32(w[j] >> 16, a.f16));
+      bad |= !(x0 < __builtin_inff()) || !(x1 < __builtin_inff());
+      big = fmaxf(big, fmaxf(x0, x1));
     }
   }
   float mul;
   const float back = query_scale(a, max_over_groups(bad ? __builtin_inff() : big), &mul);
 #pragma unroll
-  for (int o = 0; o < 2 * DB; ++o)
-    op[o] = u32x4_t{pack_f16x2(x[o][0] * mul, x[o][1] * mul), pack_f16x2(x[o][2] * mul, x[o][3] * mul),
-                    pack_f16x2(x[o][4] * mul, x[o][5] * mul), pack_f16x2(x[o][6] * mul, x[o][7] * mul)};
+  for (int o = 0; o < 2 * DB; ++o) {
+    const uint32_t w[4] = {raw[o].x, raw[o].y, raw[o].z, raw[o].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      op[o][j] = pack_f16x2(in_f32(w[j] & 0xFFFFu, a.f16) * mul, in_f32(w[j] >> 16, a.f16) * mul);
+  }
   return back;
 }
 
@@ -191,45 +228,87 @@ __device__ __forceinline__ void store_out8(const AttnArgs& a, int64_t tok, int q
 }
 
 // ------------------------------------------------------------------ the row kernel
-// A workgroup of 4 waves takes 16 NB rows of one key/value head and one chunk of keys; its
-// waves take consecutive quarters of the chunk in steps of 32 keys, codes straight from
-// memory to operands (the cache's layout: every load is one contiguous KB of a wave), the
-// next step's codes in flight while the current one is multiplied.
+// A workgroup of 4 waves takes 16 NB rows of one key/value head and a run of steps of 32 keys;
+// its waves take consecutive quarters of the run, codes straight from memory to operands
+// (the cache's layout: every load is one contiguous KB of a wave); the next step's keys are
+// loaded once the scores have used the current ones, its values after the outputs, so a
+// wave has one of the two in flight at any time (a second register set for both measured
+// no faster and costs a wave per SIMD).
+// slot < 0: the run is the whole item and the output is written; else the partial slot.
 template <int DB, int NB>
-__global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
+__device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, int s, int hk, int step0, int step1,
+                                            int64_t slot) {
   constexpr int RS = 132;  // floats of a row of the exchange buffer (128 + 4: no bank conflicts)
   __shared__ float ex[kWaves * 16 * RS];
   __shared__ float stat_m[kWaves][16 * NB], stat_l[kWaves][16 * NB];
-  int64_t id = blockIdx.x;
-  const int split = (int)(id % a.splits);
-  id /= a.splits;
-  const int tile = (int)(id % a.tiles);
-  id /= a.tiles;
-  const int hk = (int)(id % a.c.heads);
-  const int s = (int)(id / a.c.heads);
-  Tile t;
-  if (!find_tile(a, s, tile, t) || split >= t.splits) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
 
-  u32x4_t q[NB][2 * DB];
+  const int32_t c0 = t.lo + step0 * kStep, c1 = t.hi;  // (nothing is read from c1 on)
+  const int32_t steps = step1 - step0, per = (steps + kWaves - 1) / kWaves;
+  const int32_t w0 = c0 + min(steps, wave * per) * kStep, w1 = c0 + min(steps, (wave + 1) * per) * kStep;
+
+  // pages and exponents of the wave's first 64 groups of 16 keys (lane i: group i): the
+  // addresses of all that follows, so they are asked for first
+  int page = 0, ek = 0, ev = 0;
+  auto find_pages = [&](int32_t base) {
+    const int32_t pos = base + 16 * lane;
+    page = ek = ev = 0;
+    if (pos < c1) page = a.c.table[(int64_t)s * a.c.width + (pos >> a.c.tshift)];
+  };
+  auto find_exponents = [&](int32_t base) {
+    if (base + 16 * lane < c1) {
+      const bool in_pool = (uint32_t)page < (uint64_t)a.c.pages;
+      page = in_pool ? page : 0;
+      const int64_t at = (int64_t)page * a.c.heads + hk;
+      ek = in_pool ? a.c.ke[at] : 255;  // outside the pool: reads as NaN
+      ev = in_pool ? a.c.ve[at] : 255;
+    }
+  };
+  if (w0 < w1) find_pages(w0);
+
+  uint4 raw[NB][2 * DB];
   float cq[NB];
   int32_t last[NB], first[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const int row = t.r0 + 16 * nb + r;
     const bool live = row < t.r1;
-    const int i = (live ? row : t.r0) / a.group, qh = hk * a.group + (live ? row : t.r0) % a.group;
-    cq[nb] = load_query<DB>(a, a.q.p + (t.row + i) * a.q.ts + (int64_t)qh * a.q.hs, live, q[nb]);
+    const int i = (live ? row : t.r0) / a.group, qh = hk * a.group + (live ? row : t.r0) - i * a.group;
+    const uint16_t* src = a.q.p + (t.row + i) * a.q.ts + (int64_t)qh * a.q.hs;
+#pragma unroll
+    for (int o = 0; o < 2 * DB; ++o) {
+      const int d = 64 * (o >> 1) + 16 * g + 8 * (o & 1);
+      raw[nb][o] = make_uint4(0, 0, 0, 0);
+      if (live && d < a.c.dim) raw[nb][o] = *(const uint4*)(src + d);
+    }
     last[nb] = live ? last_key(a, t, i) : -1;
     first[nb] = live ? first_key(a, t, i) : 0;
   }
+  if (w0 < w1) find_exponents(w0);
   // keys that every row of the tile sees need no mask (a dead row's output is not stored)
   const int32_t all_last = last_key(a, t, t.r0 / a.group), all_first = first_key(a, t, (t.r1 - 1) / a.group);
 
-  const int32_t c0 = t.lo + split * a.chunk, c1 = (int32_t)min((int64_t)c0 + a.chunk, (int64_t)t.hi);
-  const int32_t steps = (c1 - c0 + kStep - 1) / kStep, per = (steps + kWaves - 1) / kWaves;
-  const int32_t w0 = c0 + wave * per * kStep, w1 = c0 + min(steps, (wave + 1) * per) * kStep;
+  const int64_t head_bytes = (int64_t)(64 * DB) << a.c.tshift;
+  const int slot_mask = (1 << a.c.tshift) - 1;
+  uint4 kw[2][DB], vw[2][DB];  // [group][block]
+  auto load = [&](int32_t base, int st, const uint8_t* codes, uint4 (&w)[2][DB]) {
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      const int pg = __builtin_amdgcn_readlane(page, 2 * st + gr);
+      const int64_t off = ((int64_t)pg * a.c.heads + hk) * head_bytes +
+                          (int64_t)((base + st * kStep + 16 * gr) & slot_mask) * (64 * DB) + lane * 16;
+#pragma unroll
+      for (int b = 0; b < DB; ++b) w[gr][b] = load_stream16(codes + off + b * 1024);
+    }
+  };
+  if (w0 < w1) {
+    load(w0, 0, a.c.kc, kw);
+    load(w0, 0, a.c.vc, vw);
+  }
+  u32x4_t q[NB][2 * DB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) cq[nb] = query_operands<DB>(a, raw[nb], q[nb]);
 
   f32x4_t O[NB][4 * DB];
   float m[NB], l[NB];
@@ -242,37 +321,16 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
   }
   int evr = 0;  // O is in units of 2^(evr - 127)
 
-  const int64_t head_bytes = (int64_t)(64 * DB) << a.c.tshift;
-  const int slot_mask = (1 << a.c.tshift) - 1;
   for (int32_t base = w0; base < w1; base += 64 * 16) {
-    // the next 64 groups of 16 keys: lane i holds group i's page and exponents
-    const int32_t pos = base + 16 * lane;
-    int page = 0, ek = 0, ev = 0;
-    if (pos < c1) {
-      page = a.c.table[(int64_t)s * a.c.width + (pos >> a.c.tshift)];
-      if ((uint32_t)page < (uint64_t)a.c.pages) {
-        ek = a.c.ke[(int64_t)page * a.c.heads + hk];
-        ev = a.c.ve[(int64_t)page * a.c.heads + hk];
-      } else {
-        page = 0;
-        ek = ev = 255;  // outside the pool: reads as NaN
-      }
+    if (base != w0) {
+      find_pages(base);
+      find_exponents(base);
+      load(base, 0, a.c.kc, kw);
+      load(base, 0, a.c.vc, vw);
     }
-    uint4 kw[2][2][DB], vw[2][2][DB];  // [buffer][group][block]
-    auto load = [&](int st, int buf) {
-#pragma unroll
-      for (int gr = 0; gr < 2; ++gr) {
-        const int pg = __builtin_amdgcn_readlane(page, 2 * st + gr);
-        const int64_t off = ((int64_t)pg * a.c.heads + hk) * head_bytes +
-                            (int64_t)((base + st * kStep + 16 * gr) & slot_mask) * (64 * DB) + lane * 16;
-#pragma unroll
-        for (int b = 0; b < DB; ++b) {
-          kw[buf][gr][b] = load_stream16(a.c.kc + off + b * 1024);
-          vw[buf][gr][b] = load_stream16(a.c.vc + off + b * 1024);
-        }
-      }
-    };
-    auto compute = [&](int st, int buf) {
+    const int n = min(32, (w1 - base) / kStep);
+    for (int st = 0; st < n; ++st) {
+      const int next = min(st + 1, n - 1);  // (the last step's codes again, not used)
       const int32_t key0 = base + st * kStep;
       f32x4_t S[NB][2];
 #pragma unroll
@@ -281,7 +339,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
         for (int nb = 0; nb < NB; ++nb) S[nb][gr] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
-          const uint4 w = kw[buf][gr][b];
+          const uint4 w = kw[gr][b];
           const u32x4_t k0 = {codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y)};
           const u32x4_t k1 = {codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w)};
 #pragma unroll
@@ -291,6 +349,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
           }
         }
       }
+      load(base, next, a.c.kc, kw);
       const int ek0 = __builtin_amdgcn_readlane(ek, 2 * st), ek1 = __builtin_amdgcn_readlane(ek, 2 * st + 1);
       const int ev0 = __builtin_amdgcn_readlane(ev, 2 * st), ev1 = __builtin_amdgcn_readlane(ev, 2 * st + 1);
       const float kf[2] = {scale_of(ek0), scale_of(ek1)};
@@ -338,7 +397,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int b = 0; b < DB; ++b) {
-        const uint4 x = vw[buf][0][b], y = vw[buf][1][b];
+        const uint4 x = vw[0][b], y = vw[1][b];
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -347,16 +406,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
           for (int nb = 0; nb < NB; ++nb) O[nb][4 * b + c] = mma(v, P[nb], O[nb][4 * b + c]);
         }
       }
-    };
-    const int n = min(32, (w1 - base) / kStep);
-    load(0, 0);
-    for (int st = 0; st < n; st += 2) {
-      if (st + 1 < n) load(st + 1, 1);
-      compute(st, 0);
-      if (st + 1 < n) {
-        if (st + 2 < n) load(st + 2, 0);
-        compute(st + 1, 1);
-      }
+      load(base, next, a.c.vc, vw);
     }
   }
 
@@ -370,8 +420,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
     }
   }
   __syncthreads();
-  const bool direct = t.splits == 1;
-  const int64_t all_rows = a.c.tokens * ((int64_t)a.c.heads * a.group);
+  const bool direct = slot < 0;
   const float unit = scale_of(evr);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
@@ -390,7 +439,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
       const int i = row / a.group, qh = hk * a.group + row % a.group;
       const int64_t at = (t.row + i) * ((int64_t)a.c.heads * a.group) + qh;
       const float lse2 = lg == 0.f ? kNegInf : mg + __builtin_log2f(lg) - kWeightBits;
-      if (!direct) a.part_l[split * all_rows + at] = lse2;
+      if (!direct) a.part_l[slot * a.tile_rows + 16 * nb + r] = lse2;
       else if (a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
     }
 #pragma unroll
@@ -426,17 +475,51 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(AttnArgs a) {
           v[j + 2] = f.z;
           v[j + 3] = f.w;
         }
-        const int i = row2 / a.group, qh = hk * a.group + row2 % a.group;
         if (direct) {
+          const int i = row2 / a.group, qh = hk * a.group + row2 % a.group;
           store_out8(a, t.row + i, qh, 64 * b0 + oc, v);
         } else {
-          const int64_t at = (t.row + i) * ((int64_t)a.c.heads * a.group) + qh;
-          float* po = a.part_o + (split * all_rows + at) * (64 * DB) + 64 * b0 + oc;
+          float* po = a.part_o + (slot * a.tile_rows + 16 * nb + orow) * (64 * DB) + 64 * b0 + oc;
           *(float4*)po = make_float4(v[0], v[1], v[2], v[3]);
           *(float4*)(po + 4) = make_float4(v[4], v[5], v[6], v[7]);
         }
       }
     }
+  }
+}
+
+template <int DB, int NB>
+__global__ __launch_bounds__(64 * kWaves, DB * NB <= 4 ? 2 : 1) void attn_rows_kernel(AttnArgs a) {
+  __shared__ int32_t line[kLineMax + 1];
+  Tile t;
+  if (a.shares == 0) {  // an item each
+    const int hk = (int)(blockIdx.x % a.c.heads), i = (int)(blockIdx.x / a.c.heads);
+    if (!find_tile(a, i / a.tiles, i % a.tiles, t)) return;
+    attend_rows<DB, NB>(a, t, i / a.tiles, hk, 0, steps_of(t), -1);
+    return;
+  }
+  scan_line(a, line);
+  const int n = a.c.seqs * a.tiles;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= n; i += 64 * kWaves) a.line[i] = line[i];
+  const int32_t total = line[n] * a.c.heads, share = share_of(a, total);
+  int32_t at = (int32_t)min((int64_t)blockIdx.x * share, (int64_t)total);
+  const int32_t end = (int32_t)min((int64_t)at + share, (int64_t)total);
+  while (at < end) {
+    int i = 0;  // the last one that starts at or before `at`
+    for (int d = kLineMax / 2; d > 0; d >>= 1)
+      if (i + d < n && line[i + d] * a.c.heads <= at) i += d;
+    const int32_t units = line[i + 1] - line[i], in = at - line[i] * a.c.heads;
+    const int hk = (int)((uint32_t)in / (uint32_t)units);
+    const int32_t u0 = in - hk * units, u1 = min(units, u0 + (end - at));
+    const int32_t step0 = max(u0 - kItemCost, 0), step1 = u1 - kItemCost;
+    at += u1 - u0;
+    if (step1 <= 0) continue;  // only the item's fixed cost: the next workgroup starts it
+    const int s = a.tiles == 1 ? i : i / a.tiles;
+    find_tile(a, s, i - s * a.tiles, t);
+    const int64_t slot = step0 == 0 && u1 == units ? -1 : 2 * (int64_t)blockIdx.x + (step0 == 0 ? 1 : 0);
+    attend_rows<DB, NB>(a, t, s, hk, step0, step1, slot);
+    __syncthreads();  // (the exchange buffers are used again)
   }
 }
 
@@ -522,7 +605,9 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
   const int hk = (int)(id % a.c.heads);
   const int s = (int)(id / a.c.heads);
   Tile t;
-  if (!find_tile(a, s, tile, t) || split >= t.splits) return;
+  if (!find_tile(a, s, tile, t)) return;
+  const int chunks = chunks_of(a, t);
+  if (split >= chunks) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
 
@@ -787,7 +872,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
   }
 
   // ---- outputs: 16 consecutive columns per lane and 32-column block
-  const bool direct = t.splits == 1;
+  const bool direct = chunks == 1;
   const int64_t q_heads = (int64_t)a.c.heads * a.group, all_rows = a.c.tokens * q_heads;
   const float unit = scale_of(evo);
 #pragma unroll
@@ -825,45 +910,97 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
   }
 }
 
-// ---------------------------------------------------------------- joining the splits
-// One group of 8 x blocks lanes per row: out = sum_s w_s O_s / sum_s w_s, w_s = 2^(lse_s - max).
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int per = 8 * a.c.blocks;  // threads of a row (8 columns each)
-  const int64_t id = (int64_t)blockIdx.x * (256 / per) + threadIdx.x / per;
-  const int d = (threadIdx.x % per) * 8;
-  if (threadIdx.x >= 256 / per * per) return;
-  const int64_t max_rows = (int64_t)a.c.max_tokens * a.group;
-  const int64_t rr = id % max_rows;
-  const int hk = (int)((id / max_rows) % a.c.heads);
-  const int64_t s = id / max_rows / a.c.heads;
-  if (s >= a.c.seqs) return;
+// ------------------------------------------------------------- joining partial results
+// out = sum_p w_p O_p / sum_p w_p, w_p = 2^(lse_p - max), over the pieces p of a row's keys.
+// A row takes `lanes` x 8 D64 / 64 threads: 8 columns each, every lanes-th piece; the lanes'
+// sums meet in LDS.  A workgroup holds 256 threads' worth of rows.
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int lanes) {
+  __shared__ float buf[256][11];  // 8 columns, maximum, sum (odd stride: no bank conflicts)
+  const int cols = 8 * a.c.blocks, per = cols * lanes, rows = 256 / per;  // rows of a workgroup
+  const int in_row = threadIdx.x % per, lane = in_row / cols, d = (in_row % cols) * 8;
+  const uint32_t id = blockIdx.x * rows + threadIdx.x / per, max_rows = (uint32_t)a.c.max_tokens * a.group;
+  const uint32_t item = id / max_rows, s = item / (uint32_t)a.c.heads;
+  const int rr = (int)(id - item * max_rows), hk = (int)(item - s * a.c.heads), tile = rr / a.tile_rows;
   Tile t;
-  if (!find_tile(a, (int)s, (int)(rr / a.tile_rows), t) || rr >= t.rows || t.splits == 1) return;
-  const int i = (int)rr / a.group, qh = hk * a.group + (int)rr % a.group;
-  const int64_t q_heads = (int64_t)a.c.heads * a.group, all_rows = a.c.tokens * q_heads;
-  const int64_t at = (t.row + i) * q_heads + qh;
-  float mx = kNegInf, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < t.splits; ++k) mx = fmaxf(mx, a.part_l[k * all_rows + at]);
-  for (int k = 0; k < t.splits; ++k) {
-    const float lse = a.part_l[k * all_rows + at];
-    if (lse == kNegInf) continue;  // a chunk that this row does not see
-    const float w = __builtin_amdgcn_exp2f(lse - mx);
-    sum += w;
-    const float4* p = (const float4*)(a.part_o + (k * all_rows + at) * (64 * a.c.blocks) + d);
-    const float4 x = p[0], y = p[1];
-    v[0] += w * x.x;
-    v[1] += w * x.y;
-    v[2] += w * x.z;
-    v[3] += w * x.w;
-    v[4] += w * y.x;
-    v[5] += w * y.y;
-    v[6] += w * y.z;
-    v[7] += w * y.w;
+  bool live = threadIdx.x < rows * per && s < (uint32_t)a.c.seqs && find_tile(a, (int)s, tile, t) && rr < t.rows;
+  const int64_t q_heads = (int64_t)a.c.heads * a.group;
+  int pieces = 0;
+  int64_t out_at = 0, first = 0, second = 0, step = 0;  // rows of the partial results: first, second, + step, ...
+  int i = 0, qh = 0;
+  if (live) {
+    i = rr / a.group;
+    qh = hk * a.group + rr % a.group;
+    out_at = (t.row + i) * q_heads + qh;
+    if (a.shares > 0) {
+      const int32_t v = (int)s * a.tiles + tile, total = a.line[a.c.seqs * a.tiles], before = a.line[v];
+      const int32_t share = share_of(a, total * a.c.heads), units = a.line[v + 1] - before;
+      const int32_t at = before * a.c.heads + hk * units;
+      const int32_t w0 = (uint32_t)(at + kItemCost) / (uint32_t)share, w1 = (uint32_t)(at + units - 1) / (uint32_t)share;
+      pieces = w1 - w0 + 1;
+      first = (int64_t)(2 * w0 + 1) * a.tile_rows + rr % a.tile_rows;
+      second = first + a.tile_rows;
+      step = 2 * a.tile_rows;
+    } else {
+      pieces = chunks_of(a, t);
+      step = a.c.tokens * q_heads;
+      first = out_at;
+      second = first + step;
+    }
+    live = pieces > 1;
   }
+  float mx = kNegInf, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (live) {
+    for (int k0 = lane; k0 < pieces; k0 += 4 * lanes) {  // four pieces' loads at a time
+      float lse[4];
+      float4 x[4], y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = min(k0 + u * lanes, pieces - 1);
+        const int64_t at = k == 0 ? first : second + (k - 1) * step;
+        lse[u] = a.part_l[at];
+        const float4* p = (const float4*)(a.part_o + at * (64 * a.c.blocks) + d);
+        x[u] = p[0];
+        y[u] = p[1];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (k0 + u * lanes >= pieces || lse[u] == kNegInf) continue;  // (a piece that this row does not see)
+        const float m2 = fmaxf(mx, lse[u]);
+        const float old = mx == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mx - m2);
+        const float w = __builtin_amdgcn_exp2f(lse[u] - (m2 == kNegInf ? 0.f : m2));  // (NaN stays NaN)
+        mx = m2;
+        sum = sum * old + w;
+        const float o[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * old + w * o[j];
+      }
+    }
+  }
+  if (lanes > 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) buf[threadIdx.x][j] = v[j];
+    buf[threadIdx.x][8] = mx;
+    buf[threadIdx.x][9] = sum;
+    __syncthreads();
+    if (!live || lane != 0) return;
+    for (int k = 1; k < min(lanes, pieces); ++k) {
+      const float* o = buf[threadIdx.x + k * cols];
+      const float m1 = o[8], s1 = o[9];
+      if (s1 == 0.f) continue;
+      const float m2 = fmaxf(mx, m1);
+      const float w0 = mx == kNegInf ? (sum == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mx - m2);
+      const float w1 = m1 == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m1 - m2);  // (a NaN sum without a maximum)
+      mx = m2;
+      sum = sum * w0 + s1 * w1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * w0 + o[j] * w1;
+    }
+  }
+  if (!live) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = sum == 0.f ? 0.f : v[j] / sum;
   store_out8(a, t.row + i, qh, d, v);
-  if (a.lse && d == 0) a.lse[at] = sum == 0.f ? kNegInf : (mx + __builtin_log2f(sum)) * 0.69314718055994530942f;
+  if (a.lse && d == 0) a.lse[out_at] = sum == 0.f ? kNegInf : (mx + __builtin_log2f(sum)) * 0.69314718055994530942f;
 }
 
 // NB of the row kernel: the rows of the longest sequence, as far as the registers go
@@ -875,6 +1012,9 @@ int row_blocks(const AttnArgs& a) {
   return nb;
 }
 
+// workgroups of the row kernel that a CU holds (its registers decide)
+int rows_per_cu(int blocks, int nb) { return blocks * nb <= 2 ? 3 : blocks * nb <= 4 ? 2 : 1; }
+
 // More rows than this take the tile kernel.
 constexpr int kRowKernelRows = 64;
 constexpr int kTileWaves = 8;
@@ -882,27 +1022,41 @@ int tile_row_blocks(const AttnArgs&) { return 1; }
 
 }  // namespace
 
-size_t plan_attention(AttnArgs* a, size_t ws_bytes) {
+int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
   const int64_t all = (int64_t)a->c.max_tokens * a->group;
   const bool tiled = all > kRowKernelRows;
   a->tile_rows = tiled ? 32 * tile_row_blocks(*a) * kTileWaves : 16 * row_blocks(*a);
   a->tiles = (int32_t)((all + a->tile_rows - 1) / a->tile_rows);
+  a->shares = 0;
+  a->chunk = INT32_MAX / 2;
+  a->splits = 1;
   // keys a row tile may see, rounded for its start at a multiple of 32
   const int64_t q_tokens = (a->tile_rows - 1) / a->group + 2;
   const int64_t seen = a->window > 0 ? std::min<int64_t>(a->cap, (int64_t)a->window + q_tokens) : a->cap;
   const int64_t span = (seen + 2 * kStep - 1) / kStep * kStep;
   const int64_t items = (int64_t)a->c.seqs * a->c.heads * a->tiles;
+  const int64_t most = (int64_t)(ws_bytes / ((64 * a->c.blocks + 1) * sizeof(float)));
+  if (!tiled) {
+    // as many workgroups as the CUs hold at once, none with less than a step per wave
+    const int64_t steps = items * (span / kStep);
+    const int64_t shares = std::min<int64_t>(rows_per_cu(a->c.blocks, a->tile_rows / 16) * device_cus(),
+                                             (steps + kMinShare - 1) / kMinShare);
+    const int64_t room = 2 * shares * a->tile_rows + (kLineMax / (64 * a->c.blocks) + 64) / 64 * 64;  // and the line
+    if ((int64_t)a->c.seqs * a->tiles > kLineMax || span <= kMinShare * kStep || room > most ||
+        items * (span / kStep + kItemCost) >= INT32_MAX)
+      return 0;
+    a->shares = (int32_t)shares;
+    return room;
+  }
   const int64_t rows = a->c.tokens * (int64_t)a->c.heads * a->group;
-  const size_t per = (size_t)rows * (64 * a->c.blocks + 1) * sizeof(float);
-  const int64_t unit = tiled ? 512 : kWaves * kStep;
-  int64_t splits = ((tiled ? 256 : 2048) + items - 1) / items;
+  const int64_t unit = 512;
+  int64_t splits = (256 + items - 1) / items;
   splits = std::min<int64_t>(splits, (span + unit - 1) / unit);
-  if ((size_t)splits > ws_bytes / per) splits = (int64_t)(ws_bytes / per);
-  if (splits < 2) splits = 1;
-  int64_t chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
-  a->chunk = (int32_t)std::min<int64_t>(chunk, INT32_MAX / 2);
-  a->splits = (int32_t)((span + chunk - 1) / chunk);
-  return a->splits > 1 ? per * a->splits : 0;
+  splits = std::min<int64_t>(splits, most / rows);
+  if (splits < 2) return 0;
+  a->chunk = (int32_t)(((span + splits - 1) / splits + unit - 1) / unit * unit);
+  a->splits = (int32_t)((span + a->chunk - 1) / a->chunk);
+  return a->splits > 1 ? rows * a->splits : 0;
 }
 
 wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
@@ -920,7 +1074,8 @@ wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
     }
   } else {
     const int nb = a.tile_rows / 16;
-    auto go = [&](auto kernel) { kernel<<<(unsigned)items, 64 * kWaves, 0, s>>>(a); };
+    const unsigned blocks = (unsigned)(a.shares > 0 ? a.shares : items);
+    auto go = [&](auto kernel) { kernel<<<blocks, 64 * kWaves, 0, s>>>(a); };
     switch (a.c.blocks * 8 + nb) {
       case 1 * 8 + 1: go(attn_rows_kernel<1, 1>); break;
       case 1 * 8 + 2: go(attn_rows_kernel<1, 2>); break;
@@ -936,10 +1091,15 @@ wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
     }
   }
   WQ_HIP_CHECK(hipGetLastError());
-  if (a.splits > 1) {
-    const int64_t rows = (int64_t)a.c.seqs * a.c.heads * a.c.max_tokens * a.group, per = 256 / (8 * a.c.blocks);
-    if ((rows + per - 1) / per > INT32_MAX) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
-    attn_join_kernel<<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a);
+  if (a.splits > 1 || a.shares > 0) {
+    // many pieces of few rows: a workgroup to a row; else lanes for the few pieces there are
+    const int64_t rows = (int64_t)a.c.seqs * a.c.heads * a.c.max_tokens * a.group;
+    const int cols = 8 * a.c.blocks;
+    int lanes = 1;
+    while (2 * lanes * cols <= 256 && lanes < (a.shares > 0 ? (rows <= 4096 ? 32 : 4) : a.splits)) lanes *= 2;
+    const int64_t per = 256 / (cols * lanes);
+    if (rows > INT32_MAX - 256) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
+    attn_join_kernel<<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a, lanes);
     WQ_HIP_CHECK(hipGetLastError());
   }
   return WQ_OK;

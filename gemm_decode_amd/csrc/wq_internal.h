@@ -271,14 +271,19 @@ struct AttnArgs {
   float scale_log2;   // scale * log2(e)
   int32_t tile_rows;  // rows (token, query head of one key/value head) of a row tile
   int32_t tiles;      // row tiles of the longest sequence
-  int32_t chunk;      // keys per split
-  int32_t splits;     // most splits of any row tile
-  float* part_o;      // [splits][tokens * query heads][D64]: normalised partial outputs
-  float* part_l;      // [splits][tokens * query heads]: their log2 sums
+  // how the keys are split (see wq_attn.hip): the row kernel's workgroups take equal shares
+  // of all items' steps (shares > 0: that many workgroups) or an item each; the tile kernel
+  // cuts a row tile's keys into chunks
+  int32_t shares;
+  int32_t chunk;
+  int32_t splits;     // most chunks of any row tile
+  float* part_o;      // normalised partial outputs, [slot][row][D64]
+  float* part_l;      // their log2 sums, [slot][row]
+  int32_t* line;      // with shares: the line of the items' steps, seqs * tiles + 1 positions
 };
-// Fills a's tile_rows, tiles, chunk and splits for the workspace given; returns the bytes of
-// partial results that choice takes.
-size_t plan_attention(AttnArgs* a, size_t ws_bytes);
+// Fills a's tile_rows, tiles, shares, chunk and splits for the workspace given; returns the
+// partial results' rows (of D64 + 1 floats) that choice takes.
+int64_t plan_attention(AttnArgs* a, size_t ws_bytes);
 wq_status launch_attention(const AttnArgs& a, hipStream_t s);
 
 // Device tag "<arch>:<CUs>" of the current device; empty on failure.

@@ -223,7 +223,8 @@ wq_status wq_kv_attention_workspace_size(const wq_kv_cache* cache, const wq_kv_b
     AttnArgs a{};
     const wq_status st = attn_shape(cache, batch, false, q_heads, max_kv, &a);
     if (st != WQ_OK) return st;
-    *bytes = a.c.seqs == 0 || a.c.tokens == 0 || a.c.max_tokens == 0 ? 0 : plan_attention(&a, SIZE_MAX);
+    const bool none = a.c.seqs == 0 || a.c.tokens == 0 || a.c.max_tokens == 0;
+    *bytes = none ? 0 : (size_t)plan_attention(&a, SIZE_MAX) * (64 * a.c.blocks + 1) * sizeof(float);
     return WQ_OK;
   });
 }
@@ -257,12 +258,10 @@ wq_status wq_kv_attention(const wq_kv_cache* cache, const wq_kv_batch* batch, in
     a.window = window >= INT32_MAX ? 0 : (int32_t)window;
     a.f16 = act == WQ_ACT_F16;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-    plan_attention(&a, ws ? ws_bytes : 0);
-    if (a.splits > 1) {
-      const int64_t rows = a.c.tokens * q_heads;
-      a.part_o = (float*)ws;
-      a.part_l = a.part_o + (int64_t)a.splits * rows * a.c.blocks * 64;
-    }
+    a.part_o = (float*)ws;
+    a.part_l = a.part_o + plan_attention(&a, ws ? ws_bytes : 0) * (64 * a.c.blocks);
+    // (the line of steps: the outputs' rows that no slot uses, at their end)
+    a.line = a.shares > 0 ? (int32_t*)(a.part_o + 2 * (int64_t)a.shares * a.tile_rows * (64 * a.c.blocks)) : nullptr;
     return launch_attention(a, (hipStream_t)stream);
   });
 }
