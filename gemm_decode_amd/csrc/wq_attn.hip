@@ -1092,11 +1092,12 @@ wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
   }
   WQ_HIP_CHECK(hipGetLastError());
   if (a.splits > 1 || a.shares > 0) {
-    // many pieces of few rows: a workgroup to a row; else lanes for the few pieces there are
+    // lanes for the pieces that a row has on average
     const int64_t rows = (int64_t)a.c.seqs * a.c.heads * a.c.max_tokens * a.group;
     const int cols = 8 * a.c.blocks;
     int lanes = 1;
-    while (2 * lanes * cols <= 256 && lanes < (a.shares > 0 ? (rows <= 4096 ? 32 : 4) : a.splits)) lanes *= 2;
+    const int64_t pieces = a.shares > 0 ? a.shares / (int64_t)items + 2 : a.splits;
+    while (2 * lanes * cols <= 256 && lanes < pieces) lanes *= 2;
     const int64_t per = 256 / (cols * lanes);
     if (rows > INT32_MAX - 256) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
     attn_join_kernel<<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a, lanes);

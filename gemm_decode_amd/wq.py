@@ -449,9 +449,26 @@ def wq_linear_perm(w: PackedWeight, x: torch.Tensor, perm: torch.Tensor, y: torc
 
 
 # ------------------------------------------------- rotary positions, 8-bit key/value cache
-def _same_device(*tensors) -> None:
-    dev = tensors[0].device
-    assert dev.type == "cuda" and all(t is None or t.device == dev for t in tensors), "tensors on different devices"
+# These calls take a few microseconds on the device, so the binding keeps its own share small:
+# the stream's handle is asked for directly (a torch.cuda.Stream object costs 2.7 us), the
+# descriptors are built once.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(stream, index: int):
+    """Handle of the given stream, or of the current one of device `index`."""
+    if stream is None:
+        return _raw_stream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _device_index(*tensors) -> int:
+    """Index of the GPU that holds every one of the tensors (None entries apart)."""
+    index = tensors[0].get_device()
+    assert index >= 0, "tensors must be on the GPU"
+    for t in tensors:
+        assert t is None or t.get_device() == index, "tensors on different devices"
+    return index
 
 
 def _heads3(t: torch.Tensor, what: str, dim: int | None = None):
@@ -459,19 +476,20 @@ def _heads3(t: torch.Tensor, what: str, dim: int | None = None):
     assert t.dim() == 3 and (dim is None or t.shape[2] == dim), f"{what} must be [tokens][heads][head_dim]"
     ts, hs, ds = t.stride()
     assert ds == 1 or t.shape[2] == 1, f"{what}: a head's elements must be contiguous"
-    return t.data_ptr(), ts, hs
+    return t.data_ptr() or None, ts, hs
 
 
 def _act_of(t: torch.Tensor) -> int:
-    assert t.dtype in (torch.bfloat16, torch.float16), "bf16 or fp16"
-    return _act(t)
+    dt = t.dtype
+    assert dt is torch.bfloat16 or dt is torch.float16, "bf16 or fp16"
+    return ACT["bf16"] if dt is torch.bfloat16 else ACT["f16"]
 
 
 def wq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
             axis: torch.Tensor | None = None, interleaved: bool = False, stream=None) -> None:
     """x, y bf16 or fp16 [tokens][heads][dim] (any strides; y may be x); positions int32
     [axes][tokens] or [tokens]; inv_freq fp32 [rot_dim / 2]; axis uint8 [rot_dim / 2]."""
-    _same_device(x, y, positions, inv_freq, axis)
+    index = _device_index(x, y, positions, inv_freq, axis)
     act = _act_of(x)
     assert y.dtype == x.dtype and y.shape == x.shape
     tokens, heads, dim = x.shape
@@ -483,7 +501,8 @@ def wq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, inv_freq:
     xp, xt, xh = _heads3(x, "x")
     yp, yt, yh = _heads3(y, "y")
     _check(lib.wq_rope(act, xp, xt, xh, yp, yt, yh, tokens, heads, dim, 2 * half, int(interleaved),
-                       positions.data_ptr(), axes, _ptr(axis), inv_freq.data_ptr(), _stream(stream)), "wq_rope")
+                       positions.data_ptr(), axes, None if axis is None else axis.data_ptr(), inv_freq.data_ptr(),
+                       _on(stream, index)), "wq_rope")
 
 
 def wq_kv_cache_sizes(pages: int, page_tokens: int, heads: int, head_dim: int):
@@ -495,17 +514,18 @@ def wq_kv_cache_sizes(pages: int, page_tokens: int, heads: int, head_dim: int):
 
 class KVCache:
     """A pool of pages of 8-bit keys and values (wq_kv_cache); owns its four uint8 tensors,
-    which need no initialisation."""
+    which need no initialisation and stay where they are."""
 
     def __init__(self, pages: int, page_tokens: int, heads: int, head_dim: int, device="cuda"):
         self.pages, self.page_tokens, self.heads, self.head_dim = pages, page_tokens, heads, head_dim
         cb, eb = wq_kv_cache_sizes(pages, page_tokens, heads, head_dim)
         self.k_codes, self.v_codes = (torch.empty(cb, dtype=torch.uint8, device=device) for _ in range(2))
         self.k_exps, self.v_exps = (torch.empty(eb, dtype=torch.uint8, device=device) for _ in range(2))
+        self._desc = WqKvCacheC(pages, page_tokens, heads, head_dim, 0, self.k_codes.data_ptr(),
+                                self.v_codes.data_ptr(), self.k_exps.data_ptr(), self.v_exps.data_ptr())
 
     def desc(self) -> WqKvCacheC:
-        return WqKvCacheC(self.pages, self.page_tokens, self.heads, self.head_dim, 0, self.k_codes.data_ptr(),
-                          self.v_codes.data_ptr(), self.k_exps.data_ptr(), self.v_exps.data_ptr())
+        return self._desc
 
     def nbytes(self) -> int:
         return 2 * (self.k_codes.numel() + self.k_exps.numel())
@@ -527,19 +547,24 @@ class KVBatch:
         assert table.is_contiguous(), "the page table must be contiguous"
         self.table, self.starts, self.offsets, self.max_tokens = table, starts, offsets, max_tokens
         self.seqs = seqs
+        self._desc = None
 
     def desc(self, tokens: int) -> WqKvBatchC:
-        return WqKvBatchC(self.seqs, tokens, self.max_tokens, self.table.shape[1], self.table.data_ptr(),
-                          self.starts.data_ptr(), 0 if self.offsets is None else self.offsets.data_ptr())
+        d = self._desc
+        if d is None or d.tokens != tokens:
+            d = self._desc = WqKvBatchC(self.seqs, tokens, self.max_tokens, self.table.shape[1],
+                                        self.table.data_ptr(), self.starts.data_ptr(),
+                                        0 if self.offsets is None else self.offsets.data_ptr())
+        return d
 
 
 def _kv_copy(f, where, cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream) -> None:
-    _same_device(cache.k_codes, batch.table, k, v)
+    index = _device_index(k, v, cache.k_codes, batch.table)
     act = _act_of(k)
     assert v.dtype == k.dtype and v.shape == k.shape and k.shape[1] == cache.heads
     kp, kt, kh = _heads3(k, "k", cache.head_dim)
     vp, vt, vh = _heads3(v, "v", cache.head_dim)
-    _check(f(C.byref(cache.desc()), C.byref(batch.desc(k.shape[0])), act, kp, kt, kh, vp, vt, vh, _stream(stream)),
+    _check(f(C.byref(cache.desc()), C.byref(batch.desc(k.shape[0])), act, kp, kt, kh, vp, vt, vh, _on(stream, index)),
            where)
 
 
@@ -566,7 +591,7 @@ def wq_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.
     """q, out bf16 or fp16 [tokens][q_heads][head_dim]; kv_lens int32 [seqs]; lse fp32
     [tokens][q_heads]; ws a workspace of wq_kv_attention_workspace_size bytes (or less, or None:
     the keys are then split less)."""
-    _same_device(cache.k_codes, batch.table, q, out, kv_lens, lse, ws)
+    index = _device_index(q, out, cache.k_codes, batch.table, kv_lens, lse, ws)
     act = _act_of(q)
     assert out.dtype == q.dtype and out.shape == q.shape
     assert kv_lens is None or (kv_lens.dtype == torch.int32 and kv_lens.is_contiguous()
@@ -576,8 +601,10 @@ def wq_kv_attention(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.
     qp, qt, qh = _heads3(q, "q", cache.head_dim)
     op, ot, oh = _heads3(out, "out", cache.head_dim)
     _check(lib.wq_kv_attention(C.byref(cache.desc()), C.byref(batch.desc(q.shape[0])), act, qp, qt, qh, q.shape[1],
-                               op, ot, oh, _ptr(lse), _ptr(kv_lens), max_kv, scale, int(causal), window, _ptr(ws),
-                               0 if ws is None else ws.numel(), _stream(stream)), "wq_kv_attention")
+                               op, ot, oh, None if lse is None else lse.data_ptr(),
+                               None if kv_lens is None else kv_lens.data_ptr(), max_kv, scale, int(causal), window,
+                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _on(stream, index)), "wq_kv_attention")
 
 
 # ---------------------------------------------------------------------- tuner
