@@ -159,6 +159,19 @@ __device__ __forceinline__ uint16_t round16(float v, bool f16) {
   return f16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// the largest of three (a NaN is no number), one instruction: fmaxf would first quiet every operand
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+// a copy that the compiler knows nothing about: what is computed from it inside a rare branch
+// stays there, instead of being hoisted to where every step pays for it
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // all-reduce over the four lanes of a row (l, l ^ 16, l ^ 32, l ^ 48), without LDS
 __device__ __forceinline__ float max_over_groups(float v) {
   auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -375,7 +388,7 @@ __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, in
             if (key > last[nb] || key < first[nb]) sc[e] = kNegInf;
           }
         }
-        float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+        float mx = max3(max3(sc[0], sc[1], sc[2]), max3(sc[3], sc[4], sc[5]), fmaxf(sc[6], sc[7]));
         mx = fmaxf(max_over_groups(mx), m[nb]);
         if (__builtin_amdgcn_ballot_w64(mx > m[nb]) != 0 || sink != 0) {
           const float al = mx > m[nb] ? __builtin_amdgcn_exp2f(m[nb] - mx) : 1.f;
@@ -580,9 +593,9 @@ __device__ __forceinline__ float sum_over_halves(float v) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-template <int DB, int RB, int W>
+template <int DB, int RB, int W, int KT>
 __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnArgs a, int64_t items) {
-  constexpr int KT = 64;                 // keys of a tile: 4 groups of 16
+  constexpr int MT = KT / 32, NG = KT / 16;  // 32-key blocks and 16-key groups of a tile
   constexpr int KS = 4 * DB;             // 16-column steps of a row
   constexpr int WIN = 64;                // tiles whose pages and exponents are held in LDS
   constexpr int TH = 64 * W;
@@ -590,8 +603,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
   constexpr int CK = KT * 4 * DB, CV = CK / 2;  // 16-byte chunks of a tile's keys, pairs of its values
   constexpr int NK = (CK + TH - 1) / TH, NV = (CV + TH - 1) / TH;  // of a thread
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * KB];
-  __shared__ int32_t win_page[4 * WIN];
-  __shared__ __attribute__((aligned(16))) uint8_t win_ek[4 * WIN], win_ev[4 * WIN];
+  __shared__ int32_t win_page[NG * WIN];
+  __shared__ __attribute__((aligned(16))) uint8_t win_ek[NG * WIN], win_ev[NG * WIN];
 
   // workgroups go round robin over the 8 XCDs: an XCD takes consecutive items, so the row
   // tiles of one key/value head share its L2
@@ -665,7 +678,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
   uint4 kc[NK], vc[NV][2];
   uint32_t ek4 = 0, ev4 = 0;  // exponents of the tile held in registers
   auto fill_window = [&](int j0) {  // tiles j0 .. j0 + WIN - 1
-    for (int i = tid; i < 4 * WIN; i += TH) {
+    for (int i = tid; i < NG * WIN; i += TH) {
       const int64_t pos = (int64_t)c0 + (int64_t)j0 * KT + 16 * i;
       int page = 0, ek = 0, ev = 0;
       if (pos < c1) {
@@ -684,10 +697,15 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
     }
   };
   auto load_codes = [&](int j) {
-    const int w0 = 4 * (j % WIN);
+    const int w0 = NG * (j % WIN);
     const int32_t key0 = c0 + j * KT;
-    ek4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ek[w0]);
-    ev4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ev[w0]);
+    if constexpr (NG == 4) {
+      ek4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ek[w0]);
+      ev4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ev[w0]);
+    } else {
+      ek4 = __builtin_amdgcn_readfirstlane(*(const uint16_t*)&win_ek[w0]);
+      ev4 = __builtin_amdgcn_readfirstlane(*(const uint16_t*)&win_ev[w0]);
+    }
     // key chunks in the order [group][block][lane], value pairs [group][block][g % 2][column]
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
@@ -716,7 +734,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
     v_bytes = ev4;
     v_bad = false;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) v_bad |= ((ev4 >> (8 * g)) & 0xFF) == 0xFF;
+    for (int g = 0; g < NG; ++g) v_bad |= ((ev4 >> (8 * g)) & 0xFF) == 0xFF;
     uint8_t* kd = lds[buf];
     uint8_t* vd = lds[buf] + KB;
 #pragma unroll
@@ -776,9 +794,9 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
     if (key0 <= some_last && key0 + KT > some_first) {
       const uint8_t* kd = lds[j & 1] + lane * 16;
       const uint8_t* vd = kd + KB;
-      f32x16_t S[RB][2];
+      f32x16_t S[RB][MT];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -794,23 +812,27 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
       const int sink = evo - evt;  // <= 0
       evo = evt;
       const float o_shift = sink <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + sink) << 23);
-      u32x4_t P[RB][4];
+      u32x4_t P[RB][NG];
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         // (held above 0: a masked -infinity stays one)
         const float c0 = scale_of(ekt) * cq[rb], tiny = __uint_as_float(1u << 23), c = c0 < tiny ? tiny : c0;
         if (mask) {
+          // key - (key0 + 4 h) lies in lo .. hi for the row's keys
+          const int32_t at = opaque(key0 + 4 * h), lo = first[rb] - at, hi = last[rb] - at;
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int32_t key = key0 + 32 * mt + 8 * (e >> 2) + 4 * h + (e & 3);
-              if (key > last[rb] || key < first[rb]) S[rb][mt][e] = kNegInf;
+              const int32_t k = 32 * mt + 8 * (e >> 2) + (e & 3);
+              if (k > hi || k < lo) S[rb][mt][e] = kNegInf;
             }
         }
         float mx = kNegInf;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fmaxf(S[rb][0][e], S[rb][1][e]));
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) mx = max3(mx, S[rb][mt][e], S[rb][mt][e + 1]);
         mx = fmaxf(max_over_halves(mx) * c, m[rb]);
         if (__builtin_amdgcn_ballot_w64(mx > m[rb]) != 0 || sink != 0) {
           const float al = mx > m[rb] ? __builtin_amdgcn_exp2f(m[rb] - mx) : 1.f;
@@ -825,7 +847,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
         const float bias = kWeightBits - (m[rb] == kNegInf ? 0.f : m[rb]);
         float sum = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             S[rb][mt][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[rb][mt][e], c, bias));
@@ -833,23 +855,19 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
           }
         l[rb] += sum;
         if (poisoned) {  // a row that sees a key of a poisoned value page is NaN
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int32_t key = key0 + 32 * mt + 8 * (e >> 2) + 4 * h + (e & 3);
-              if (((ev_bytes >> (8 * (2 * mt + (e >> 3)))) & 0xFF) == 0xFF && key <= last[rb] && key >= first[rb])
-                l[rb] = __builtin_nanf("");
-            }
+          const int32_t at = opaque(key0);
+          for (int g = 0; g < NG; ++g)
+            if (((ev_bytes >> (8 * g)) & 0xFF) == 0xFF && first[rb] < at + 16 * (g + 1) && last[rb] >= at + 16 * g)
+              l[rb] = __builtin_nanf("");
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
           for (int j2 = 0; j2 < 4; ++j2)
             P[rb][g][j2] = pack_f16x2(S[rb][g >> 1][8 * (g & 1) + 2 * j2], S[rb][g >> 1][8 * (g & 1) + 2 * j2 + 1]);
       }
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int o = 0; o < 2 * DB; ++o) {
           const u32x4_t vf = *(const u32x4_t*)(vd + (g * 2 * DB + o) * 1024);
@@ -1015,6 +1033,8 @@ int row_blocks(const AttnArgs& a) {
 // workgroups of the row kernel that a CU holds (its registers decide)
 int rows_per_cu(int blocks, int nb) { return blocks * nb <= 2 ? 3 : blocks * nb <= 4 ? 2 : 1; }
 
+constexpr int64_t kTileCost = 192;
+
 // More rows than this take the tile kernel.
 constexpr int kRowKernelRows = 64;
 constexpr int kTileWaves = 8;
@@ -1048,13 +1068,19 @@ int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
     a->shares = (int32_t)shares;
     return room;
   }
-  const int64_t rows = a->c.tokens * (int64_t)a->c.heads * a->group;
-  const int64_t unit = 512;
-  int64_t splits = (256 + items - 1) / items;
-  splits = std::min<int64_t>(splits, (span + unit - 1) / unit);
-  splits = std::min<int64_t>(splits, most / rows);
-  if (splits < 2) return 0;
-  a->chunk = (int32_t)(((span + splits - 1) / splits + unit - 1) / unit * unit);
+  // The split whose rounds of workgroups over the CUs take least: a round costs its keys and
+  // kTileCost keys' worth of queries and outputs (with partial results, twice that).
+  const int64_t rows = a->c.tokens * (int64_t)a->c.heads * a->group, cus = device_cus();
+  int64_t best = 1, best_cost = (items + cus - 1) / cus * (span + kTileCost);
+  for (int64_t n = 2; n <= 16 && rows * n <= most; ++n) {
+    const int64_t chunk = (span + n - 1) / n, cost = (items * n + cus - 1) / cus * (chunk + 2 * kTileCost);
+    if (chunk >= 256 && cost < best_cost) {
+      best = n;
+      best_cost = cost;
+    }
+  }
+  if (best < 2) return 0;
+  a->chunk = (int32_t)(((span + best - 1) / best + 63) / 64 * 64);
   a->splits = (int32_t)((span + a->chunk - 1) / a->chunk);
   return a->splits > 1 ? rows * a->splits : 0;
 }
@@ -1066,10 +1092,10 @@ wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
     const unsigned blocks = (unsigned)((items + 7) / 8 * 8);
     auto go = [&](auto kernel) { kernel<<<blocks, 64 * kTileWaves, 0, s>>>(a, (int64_t)items); };
     switch (a.c.blocks) {
-      case 1: go(attn_tile_kernel<1, 1, kTileWaves>); break;
-      case 2: go(attn_tile_kernel<2, 1, kTileWaves>); break;
-      case 3: go(attn_tile_kernel<3, 1, kTileWaves>); break;
-      case 4: go(attn_tile_kernel<4, 1, kTileWaves>); break;
+      case 1: go(attn_tile_kernel<1, 1, kTileWaves, 64>); break;
+      case 2: go(attn_tile_kernel<2, 1, kTileWaves, 64>); break;
+      case 3: go(attn_tile_kernel<3, 1, kTileWaves, 32>); break;
+      case 4: go(attn_tile_kernel<4, 1, kTileWaves, 32>); break;
       default: return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: no kernel for this head_dim");
     }
   } else {
