@@ -594,7 +594,7 @@ __device__ __forceinline__ float sum_over_halves(float v) {
 }
 
 template <int DB, int RB, int W, int KT>
-__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnArgs a, int64_t items) {
+__global__ __launch_bounds__(64 * W, DB == 1 ? 4 : 2) void attn_tile_kernel(AttnArgs a, uint32_t pairs, bool spread) {
   constexpr int MT = KT / 32, NG = KT / 16;  // 32-key blocks and 16-key groups of a tile
   constexpr int KS = 4 * DB;             // 16-column steps of a row
   constexpr int WIN = 64;                // tiles whose pages and exponents are held in LDS
@@ -606,17 +606,25 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attn_tile_kernel(AttnA
   __shared__ int32_t win_page[NG * WIN];
   __shared__ __attribute__((aligned(16))) uint8_t win_ek[NG * WIN], win_ev[NG * WIN];
 
-  // workgroups go round robin over the 8 XCDs: an XCD takes consecutive items, so the row
-  // tiles of one key/value head share its L2
-  const int64_t per_xcd = (items + 7) / 8;
-  int64_t id = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if (id >= items || (int64_t)(blockIdx.x >> 3) >= per_xcd) return;
-  const int tile = a.tiles - 1 - (int)(id % a.tiles);  // the rows that see most come first
-  id /= a.tiles;
-  const int split = (int)(id % a.splits);
-  id /= a.splits;
-  const int hk = (int)(id % a.c.heads);
-  const int s = (int)(id / a.c.heads);
+  // Workgroups go round robin over the 8 XCDs.  A pair (sequence, key/value head, chunk) keeps
+  // its row tiles on one XCD, whose L2 then holds its codes, the tiles that see most first;
+  // pairs too few to load the XCDs alike share all of them in runs of consecutive tiles.
+  const int xcd = blockIdx.x & 7;
+  int tile;
+  uint32_t pair = 0;
+  if (spread) {
+    const uint32_t per_xcd = (pairs * a.tiles + 7) / 8, k = blockIdx.x >> 3, item = xcd * per_xcd + k;
+    pair = item / (uint32_t)a.tiles;
+    tile = a.tiles - 1 - (int)(item - pair * a.tiles);
+    if (k >= per_xcd || pair >= pairs) return;
+  } else {
+    const uint32_t per_xcd = (pairs + 7) / 8, k = blockIdx.x >> 3, back = k / per_xcd;
+    pair = (k - back * per_xcd) * 8 + xcd;
+    tile = a.tiles - 1 - (int)back;
+    if (pair >= pairs) return;
+  }
+  const uint32_t sh = pair / (uint32_t)a.splits;
+  const int split = (int)(pair - sh * a.splits), s = (int)(sh / (uint32_t)a.c.heads), hk = (int)(sh - (uint32_t)s * a.c.heads);
   Tile t;
   if (!find_tile(a, s, tile, t)) return;
   const int chunks = chunks_of(a, t);
@@ -1087,10 +1095,12 @@ int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
 
 wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
   const __int128 items = (__int128)a.c.seqs * a.c.heads * a.tiles * a.splits;
-  if (items > INT32_MAX - 8) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
+  if (items > INT32_MAX - 8 * (__int128)a.tiles) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
   if ((int64_t)a.c.max_tokens * a.group > kRowKernelRows) {
-    const unsigned blocks = (unsigned)((items + 7) / 8 * 8);
-    auto go = [&](auto kernel) { kernel<<<blocks, 64 * kTileWaves, 0, s>>>(a, (int64_t)items); };
+    const uint32_t pairs = (uint32_t)(items / a.tiles);
+    const bool spread = pairs % 8 != 0 && pairs < 64;
+    const unsigned blocks = (unsigned)(spread ? (items + 7) / 8 * 8 : (int64_t)(pairs + 7) / 8 * 8 * a.tiles);
+    auto go = [&](auto kernel) { kernel<<<blocks, 64 * kTileWaves, 0, s>>>(a, pairs, spread); };
     switch (a.c.blocks) {
       case 1: go(attn_tile_kernel<1, 1, kTileWaves, 64>); break;
       case 2: go(attn_tile_kernel<2, 1, kTileWaves, 64>); break;
