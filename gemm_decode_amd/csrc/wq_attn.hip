@@ -24,6 +24,7 @@
 // Where the row tiles alone leave CUs idle or unevenly busy, their keys are split and a second
 // kernel joins the partial outputs (normalised, with their log2 sums).
 #include <algorithm>
+#include <type_traits>
 
 #include "wq_internal.h"
 
@@ -31,6 +32,7 @@ namespace wq {
 namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
@@ -186,47 +188,37 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-__device__ __forceinline__ float in_f32(uint32_t bits, bool f16) {
-  return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : __uint_as_float(bits << 16);
-}
-// *mul: the power of two that puts a row of largest magnitude `big` below 2^15 (with the sign
-// of the softmax scale, so that what is returned is not negative): 2^(14 - floor(log2 big)),
-// held to normal numbers.  Returns what takes it out of the score, times |scale| log2 e; NaN
-// for a row that is not finite (every score of it is then infinite or NaN, and so is the row).
-__device__ __forceinline__ float query_scale(const AttnArgs& a, float big, float* mul) {
-  const int E = (int)(__float_as_uint(big) >> 23);
-  const int up = E == 255 ? 127 : min(268 - E, 253);
-  const float f = __uint_as_float((uint32_t)up << 23);
-  *mul = a.scale_log2 < 0.f ? -f : f;
-  return E == 255 ? __builtin_nanf("") : __uint_as_float((uint32_t)(254 - up) << 23) * __builtin_fabsf(a.scale_log2);
-}
-
-// Query rows as fp16 operands: lane (r = lane % 16, g = lane / 16) holds row r, columns 64 b
-// + 16 g + 8 s + j in raw[2 b + s].  Returns query_scale's factor.
-template <int DB>
-__device__ __forceinline__ float query_operands(const AttnArgs& a, const uint4 (&raw)[2 * DB], u32x4_t (&op)[2 * DB]) {
-  float big = 0.f;
-  bool bad = false;
+// A query row's elements as this lane holds them (N x 8) into fp16 operands.  The row is
+// scaled by the power of two that puts its largest magnitude below 2^15 (2^(14 - floor(log2
+// max)), held to normal numbers), with the sign of the softmax scale; returned is what takes
+// that out of the score, times |scale| log2 e: not negative, NaN for a row that is not
+// finite (every score of it is then infinite or NaN, and so is the row).  `across` joins the
+// largest magnitude's bits over the lanes of a row.
+template <bool F16, int N, class Across>
+__device__ __forceinline__ float query_operands_of(const AttnArgs& a, const uint4 (&raw)[N], u32x4_t (&op)[N], Across across) {
+  auto f32 = [](uint32_t b) { return F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)b) : __uint_as_float(b << 16); };
+  u16x2_t m = {0, 0};
 #pragma unroll
-  for (int o = 0; o < 2 * DB; ++o) {
+  for (int o = 0; o < N; ++o) {
     const uint32_t w[4] = {raw[o].x, raw[o].y, raw[o].z, raw[o].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x0 = __builtin_fabsf(in_f32(w[j] & 0xFFFFu, a.f16)), x1 = __builtin_fabsf(in_f32(w[j] >> 16, a.f16));
-      bad |= !(x0 < __builtin_inff()) || !(x1 < __builtin_inff());
-      big = fmaxf(big, fmaxf(x0, x1));
-    }
+    for (int j = 0; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[j] & 0x7FFF7FFFu));
   }
-  float mul;
-  const float back = query_scale(a, max_over_groups(bad ? __builtin_inff() : big), &mul);
+  const uint32_t big = across(max((uint32_t)m.x, (uint32_t)m.y));
+  const bool bad = big >= (F16 ? 0x7C00u : 0x7F80u);
+  const int E = (int)(__float_as_uint(f32(big)) >> 23), up = bad ? 127 : min(268 - E, 253);
+  const float pos = __uint_as_float((uint32_t)up << 23), mul = a.scale_log2 < 0.f ? -pos : pos;
 #pragma unroll
-  for (int o = 0; o < 2 * DB; ++o) {
+  for (int o = 0; o < N; ++o) {
     const uint32_t w[4] = {raw[o].x, raw[o].y, raw[o].z, raw[o].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      op[o][j] = pack_f16x2(in_f32(w[j] & 0xFFFFu, a.f16) * mul, in_f32(w[j] >> 16, a.f16) * mul);
+    for (int j = 0; j < 4; ++j) op[o][j] = pack_f16x2(f32(w[j] & 0xFFFFu) * mul, f32(w[j] >> 16) * mul);
   }
-  return back;
+  return bad ? __builtin_nanf("") : __uint_as_float((uint32_t)(254 - up) << 23) * __builtin_fabsf(a.scale_log2);
+}
+template <int N, class Across>
+__device__ __forceinline__ float query_operands(const AttnArgs& a, const uint4 (&raw)[N], u32x4_t (&op)[N], Across across) {
+  return a.f16 ? query_operands_of<true>(a, raw, op, across) : query_operands_of<false>(a, raw, op, across);
 }
 
 // Where a finished row goes: 8 columns from d on, v already the row's output (or normalised
@@ -321,7 +313,8 @@ __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, in
   }
   u32x4_t q[NB][2 * DB];
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) cq[nb] = query_operands<DB>(a, raw[nb], q[nb]);
+  for (int nb = 0; nb < NB; ++nb)  // lanes l, l ^ 16, l ^ 32, l ^ 48 share a row
+    cq[nb] = query_operands(a, raw[nb], q[nb], [](uint32_t v) { return (uint32_t)max_over_groups((float)v); });
 
   f32x4_t O[NB][4 * DB];
   float m[NB], l[NB];
@@ -537,11 +530,28 @@ __global__ __launch_bounds__(64 * kWaves, DB * NB <= 4 ? 2 : 1) void attn_rows_k
 }
 
 // ----------------------------------------------------------------- the tile kernel
-// Many rows per key/value head (prompts): a workgroup of W waves takes 32 RB W rows and walks
-// the keys in tiles of KT.  The waves decode a tile's codes together into fp16 operands in
-// LDS, once for all rows and one tile ahead (two buffers, the codes of the tile after that
-// in flight in registers), so decoding costs a row little; every wave then multiplies its own
-// 32 RB rows by the whole tile on v_mfma_f32_32x32x16_f16.
+// Many rows per key/value head (prompts): a workgroup of 8 waves takes 256 rows, 32 to a
+// wave, and walks the keys in tiles of KT.  The waves decode a tile's codes together into
+// fp16 operands in LDS, once for all rows, the codes of the next tile in flight in
+// registers; every wave multiplies its own rows by the whole tile on
+// v_mfma_f32_32x32x16_f16.
+//
+// The matrix cores and the vector units take about the same time for a tile (D = 128, 64
+// keys and 32 rows: 32 products of 32 cycles; 32 weights per lane at some 28 cycles, and the
+// decoding), so the two halves of the workgroup, one wave each on every SIMD, alternate:
+// while waves 0-3 multiply (O += P V of the tile before, S = Q K of this one), waves 4-7
+// form weights, and the other way round, with a barrier between the phases.
+// With all eight in step both units stood idle half of the time (8192-token prompt, 32 over
+// 8 heads of 128: 622 us against TILE_FIG).
+//   phase 2 j      waves 0-3: multiply (j)     waves 4-7: weights (j - 1)
+//   phase 2 j + 1  waves 0-3: weights (j)      waves 4-7: multiply (j)
+// A wave issues about one instruction in 5 cycles, whatever its kind, and a taken branch costs
+// it some 100: the phase of weights is kept to these, with what is rare out of line, and
+// the decoding and all bookkeeping stand between the products of the other phase.
+// multiply (j) reads the keys of tile j and the values of tile j - 1 and writes the keys of j
+// + 1 and the values of j (each half of the workgroup its share), so two buffers of each
+// suffice: what a phase writes was last read in the phase before, what it reads was
+// written by then.
 //
 // LDS holds operands in lane order, 1 KB blocks of 16 bytes per lane: a read is one ds_read_b128
 // over contiguous KB, without bank conflicts.  Keys: block (32 keys, 16 columns), lane (r, h)
@@ -565,8 +575,11 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, f16x2_t m, f16x2_t c) 
 // q 2^d of four codes: lo and hi pair
 struct Decode {
   f16x2_t mul, sub;  // 2^d, -1152 2^d
+  Decode() = default;
   __device__ __forceinline__ Decode(int e, int ref) {  // e, ref: exponent bytes; e 255: NaN
-    const float f = e == 255 ? __builtin_nanf("") : e - ref < -24 ? 0.f : __uint_as_float((uint32_t)(127 + e - ref) << 23);
+    // (below 2^-24 the conversion gives 0)
+    const uint32_t bits = (uint32_t)max(127 + e - ref, 0) << 23;
+    const float f = __uint_as_float(bits | (e == 255 ? 0x7FC00000u : 0u));
     mul = f16x2_t{(_Float16)f, (_Float16)f};
     sub = mul * f16x2_t{(_Float16)-1152.f, (_Float16)-1152.f};
   }
@@ -593,18 +606,21 @@ __device__ __forceinline__ float sum_over_halves(float v) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-template <int DB, int RB, int W, int KT>
-__global__ __launch_bounds__(64 * W, DB == 1 ? 4 : 2) void attn_tile_kernel(AttnArgs a, uint32_t pairs, bool spread) {
+constexpr int kTileWaves = 8;
+
+template <int DB, int KT>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs a, uint32_t pairs,
+                                                                                     bool spread) {
   constexpr int MT = KT / 32, NG = KT / 16;  // 32-key blocks and 16-key groups of a tile
-  constexpr int KS = 4 * DB;             // 16-column steps of a row
-  constexpr int WIN = 64;                // tiles whose pages and exponents are held in LDS
-  constexpr int TH = 64 * W;
-  constexpr int KB = KT * 64 * DB * 2;   // bytes of a tile's keys (or values) as fp16
-  constexpr int CK = KT * 4 * DB, CV = CK / 2;  // 16-byte chunks of a tile's keys, pairs of its values
-  constexpr int NK = (CK + TH - 1) / TH, NV = (CV + TH - 1) / TH;  // of a thread
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * KB];
-  __shared__ int32_t win_page[NG * WIN];
-  __shared__ __attribute__((aligned(16))) uint8_t win_ek[NG * WIN], win_ev[NG * WIN];
+  constexpr int KS = 4 * DB;                 // 16-column steps of a row
+  constexpr int WIN = 64;                    // the pages and exponents of 2 WIN tiles are held in LDS
+  constexpr int TH = 64 * kTileWaves;
+  constexpr int KB = KT * 64 * DB * 2;       // bytes of a tile's keys (or values) as fp16
+  constexpr int CH = KT * 4 * DB;            // 16-byte chunks of a tile's keys (or values)
+  static_assert(CH <= TH, "a thread decodes one chunk of each");
+  __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][KB], lds_v[2][KB];
+  __shared__ int64_t win_at[2 * WIN * NG];
+  __shared__ __attribute__((aligned(16))) uint8_t win_ek[2 * WIN * NG], win_ev[2 * WIN * NG];
 
   // Workgroups go round robin over the 8 XCDs.  A pair (sequence, key/value head, chunk) keeps
   // its row tiles on one XCD, whose L2 then holds its codes, the tiles that see most first;
@@ -631,62 +647,14 @@ __global__ __launch_bounds__(64 * W, DB == 1 ? 4 : 2) void attn_tile_kernel(Attn
   if (split >= chunks) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-
-  // ---- this wave's rows
-  const int wr0 = t.r0 + 32 * RB * wave, wr1 = min(wr0 + 32 * RB, t.r1);
-  u32x4_t q[RB][KS];
-  float cq[RB];
-  int32_t last[RB], first[RB];
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    const int row = wr0 + 32 * rb + r;
-    const bool live = row < t.r1;
-    const int i = (live ? row : t.r0) / a.group, qh = hk * a.group + (live ? row : t.r0) % a.group;
-    const uint16_t* src = a.q.p + (t.row + i) * a.q.ts + (int64_t)qh * a.q.hs;
-    uint4 raw[KS];
-    float big = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int d = 16 * k + 8 * h;
-      raw[k] = make_uint4(0, 0, 0, 0);
-      if (live && d < a.c.dim) raw[k] = *(const uint4*)(src + d);
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x0 = __builtin_fabsf(in_f32(w[j] & 0xFFFFu, a.f16)), x1 = __builtin_fabsf(in_f32(w[j] >> 16, a.f16));
-        bad |= !(x0 < __builtin_inff()) || !(x1 < __builtin_inff());
-        big = fmaxf(big, fmaxf(x0, x1));
-      }
-    }
-    float mul;
-    cq[rb] = query_scale(a, max_over_halves(bad ? __builtin_inff() : big), &mul);
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        q[rb][k][j] = pack_f16x2(in_f32(w[j] & 0xFFFFu, a.f16) * mul, in_f32(w[j] >> 16, a.f16) * mul);
-    }
-    last[rb] = live ? last_key(a, t, i) : -1;
-    first[rb] = live ? first_key(a, t, i) : 0;
-  }
-  // keys that some row, and that every row, of this wave sees
-  const bool any_row = wr0 < t.r1;
-  const int i_lo = (any_row ? wr0 : t.r0) / a.group, i_hi = any_row ? (wr1 - 1) / a.group : i_lo;
-  const int32_t some_last = any_row ? last_key(a, t, i_hi) : -1, some_first = first_key(a, t, i_lo);
-  const int32_t all_last = last_key(a, t, i_lo), all_first = first_key(a, t, i_hi);
+  const bool late = wave >= kTileWaves / 2;  // the half that lags a phase
 
   const int32_t c0 = t.lo + split * a.chunk, c1 = (int32_t)min((int64_t)c0 + a.chunk, (int64_t)t.hi);
   const int32_t tiles = (c1 - c0 + KT - 1) / KT;
 
-  // ---- codes of a tile: memory -> registers -> fp16 operands in LDS
-  const int64_t head_bytes = (int64_t)(64 * DB) << a.c.tshift;
-  const int slot_mask = (1 << a.c.tshift) - 1;
-  uint4 kc[NK], vc[NV][2];
-  uint32_t ek4 = 0, ev4 = 0;  // exponents of the tile held in registers
-  auto fill_window = [&](int j0) {  // tiles j0 .. j0 + WIN - 1
-    for (int i = tid; i < NG * WIN; i += TH) {
+  // ---- places and exponents of the groups of tiles j0 .. j0 + n - 1 (a ring of 2 WIN tiles)
+  auto fill_window = [&](int j0, int n) {
+    for (int i = tid; i < NG * n; i += TH) {
       const int64_t pos = (int64_t)c0 + (int64_t)j0 * KT + 16 * i;
       int page = 0, ek = 0, ev = 0;
       if (pos < c1) {
@@ -699,239 +667,292 @@ __global__ __launch_bounds__(64 * W, DB == 1 ? 4 : 2) void attn_tile_kernel(Attn
           ek = ev = 255;  // outside the pool: reads as NaN
         }
       }
-      win_page[i] = page;
-      win_ek[i] = (uint8_t)ek;
-      win_ev[i] = (uint8_t)ev;
+      const int at = (j0 * NG + i) % (2 * WIN * NG);
+      win_at[at] = ((int64_t)page * a.c.heads + hk) * ((int64_t)(64 * DB) << a.c.tshift) +
+                   (pos & ((1 << a.c.tshift) - 1)) * (64 * DB);
+      win_ek[at] = (uint8_t)ek;
+      win_ev[at] = (uint8_t)ev;
     }
   };
-  auto load_codes = [&](int j) {
-    const int w0 = NG * (j % WIN);
-    const int32_t key0 = c0 + j * KT;
-    if constexpr (NG == 4) {
-      ek4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ek[w0]);
-      ev4 = __builtin_amdgcn_readfirstlane(*(const uint32_t*)&win_ev[w0]);
-    } else {
-      ek4 = __builtin_amdgcn_readfirstlane(*(const uint16_t*)&win_ek[w0]);
-      ev4 = __builtin_amdgcn_readfirstlane(*(const uint16_t*)&win_ev[w0]);
-    }
-    // key chunks in the order [group][block][lane], value pairs [group][block][g % 2][column]
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int ch = tid + TH * i, gr = ch / (64 * DB);
-      if (CK % TH != 0 && ch >= CK) break;
-      const int64_t off = ((int64_t)win_page[w0 + gr] * a.c.heads + hk) * head_bytes +
-                          (int64_t)((key0 + 16 * gr) & slot_mask) * (64 * DB) + (ch % (64 * DB)) * 16;
-      kc[i] = *(const uint4*)(a.c.kc + off);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int pr = tid + TH * i, gr = pr / (32 * DB), in = pr % (32 * DB);
-      if (CV % TH != 0 && pr >= CV) break;
-      const int64_t off = ((int64_t)win_page[w0 + gr] * a.c.heads + hk) * head_bytes +
-                          (int64_t)((key0 + 16 * gr) & slot_mask) * (64 * DB) + (in / 32) * 1024 + (in % 32) * 16;
-      vc[i][0] = *(const uint4*)(a.c.vc + off);
-      vc[i][1] = *(const uint4*)(a.c.vc + off + 512);
-    }
+  auto exponents = [&](const uint8_t* win, int j) -> uint32_t {  // the bytes of a tile's groups
+    const uint8_t* p = win + NG * (j % (2 * WIN));
+    return NG == 4 ? *(const uint32_t*)p : (uint32_t) * (const uint16_t*)p;
   };
-  int ek_tile = 0, evr = 0;  // reference exponents of the tile last decoded
-  bool v_bad = false;        // it holds a poisoned value page
-  uint32_t v_bytes = 0;
-  auto decode = [&](int buf) {
-    ek_tile = largest_exponent(ek4);
-    evr = max(evr, largest_exponent(ev4));
-    v_bytes = ev4;
-    v_bad = false;
+  if (tiles > 0) fill_window(0, 2 * WIN);
+
+  // ---- this wave's rows
+  const int wr0 = t.r0 + 32 * wave, wr1 = min(wr0 + 32, t.r1), row = wr0 + r;
+  const bool live = row < t.r1;
+  u32x4_t q[KS];
+  float cq;
+  int32_t last, first;
+  {
+    const int i = (live ? row : t.r0) / a.group, qh = hk * a.group + (live ? row : t.r0) - i * a.group;
+    const uint16_t* src = a.q.p + (t.row + i) * a.q.ts + (int64_t)qh * a.q.hs;
+    uint4 raw[KS];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) v_bad |= ((ev4 >> (8 * g)) & 0xFF) == 0xFF;
-    uint8_t* kd = lds[buf];
-    uint8_t* vd = lds[buf] + KB;
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int ch = tid + TH * i, gr = ch / (64 * DB), in = ch % (64 * DB);
-      if (CK % TH != 0 && ch >= CK) break;
-      const int ks = 4 * (in / 64) + (in % 64) / 16, key = 16 * gr + in % 16;
-      const Decode dec((ek4 >> (8 * gr)) & 0xFF, ek_tile);
-      const uint2 x = dec(kc[i].x), y = dec(kc[i].y), z = dec(kc[i].z), w = dec(kc[i].w);
-      uint8_t* d = kd + ((key / 32) * KS + ks) * 1024 + (key % 32) * 16;
-      *(uint4*)d = make_uint4(x.x, x.y, y.x, y.y);
-      *(uint4*)(d + 512) = make_uint4(z.x, z.y, w.x, w.y);
+    for (int k = 0; k < KS; ++k) {
+      const int d = 16 * k + 8 * h;
+      raw[k] = make_uint4(0, 0, 0, 0);
+      if (live && d < a.c.dim) raw[k] = *(const uint4*)(src + d);
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int pr = tid + TH * i, gr = pr / (32 * DB), in = pr % (32 * DB);
-      if (CV % TH != 0 && pr >= CV) break;
-      const int e = (ev4 >> (8 * gr)) & 0xFF, g = (in % 32) / 16, c = in % 16;
-      const Decode dec(e == 255 ? 0 : e, evr);  // (a poisoned page is told to the rows that see it)
-      uint8_t* d = vd + (gr * 2 * DB + 2 * (in / 32) + c / 8) * 1024 + g * 512 + (c % 8) * 16;
-      const uint32_t lo[4] = {vc[i][0].x, vc[i][0].y, vc[i][0].z, vc[i][0].w};
-      const uint32_t hi[4] = {vc[i][1].x, vc[i][1].y, vc[i][1].z, vc[i][1].w};
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const uint2 x = dec(lo[m]), y = dec(hi[m]);
-        *(uint4*)(d + m * 128) = make_uint4(x.x, x.y, y.x, y.y);
+    // lanes l and l ^ 32 share a row
+    cq = query_operands(a, raw, q, [](uint32_t v) { return (uint32_t)max_over_halves((float)v); });
+    last = live ? last_key(a, t, i) : -1;
+    first = live ? first_key(a, t, i) : 0;
+  }
+  // keys that some row, and that every row, of this wave sees
+  const bool any_row = wr0 < t.r1;
+  const int i_lo = (any_row ? wr0 : t.r0) / a.group, i_hi = any_row ? (wr1 - 1) / a.group : i_lo;
+  const int32_t some_last = any_row ? last_key(a, t, i_hi) : -1, some_first = first_key(a, t, i_lo);
+  const int32_t all_last = last_key(a, t, i_lo), all_first = first_key(a, t, i_hi);
+
+  // ---- codes of a tile: memory -> registers -> fp16 operands in LDS
+  // A thread takes one chunk of the keys and one of the values, in the order [group][block]
+  // [lane]; where there are more threads than chunks, some take the same one (a branch taken
+  // costs a lone wave some 100 cycles, more than the decoding).  Nothing below asks whether a
+  // tile exists: past the last one the window names page 0 and nobody uses what is decoded.
+  const int ch = tid % CH, c_group = ch / (64 * DB), c_in = ch % (64 * DB), c_lane = c_in % 64;
+  const uint8_t *k_src = a.c.kc + c_in * 16, *v_src = a.c.vc + c_in * 16;
+  const int k_dst = ((c_group / 2) * KS + 4 * (c_in / 64) + c_lane / 16) * 1024 + ((c_group & 1) * 16 + c_lane % 16) * 16;
+  const int v_dst = (c_group * 2 * DB + 2 * (c_in / 64) + (c_lane % 16) / 8) * 1024 + ((c_lane / 16) & 1) * 512 +
+                    (c_lane % 8) * 16 + (c_lane / 32) * 8;
+  uint4 kc, vc;
+  int64_t key_at, value_at;
+  auto find_keys = [&](int j) { key_at = win_at[NG * (j % (2 * WIN)) + c_group]; };
+  auto find_values = [&](int j) { value_at = win_at[NG * (j % (2 * WIN)) + c_group]; };
+  // Exponent bytes of the keys of tile j + 1 (what stage (j) decodes) and of the values of tile
+  // j, and the largest value exponent up to there.
+  uint32_t ek_0 = 0, ev_0 = 0;
+  int evr = 0;
+  uint32_t ek_next = 0, ev_next = 0;
+  // what stage (j) needs from the window, asked for ahead
+  auto ask = [&](int j) {
+    ek_next = exponents(win_ek, j + 1);
+    ev_next = exponents(win_ev, j);
+    find_keys(j + 2);
+    find_values(j + 1);
+  };
+  // this thread's share of the keys of tile j + 1 and the values of tile j, in STAGE steps that
+  // stand between the products: a word of codes each, then the codes of what is staged next
+  constexpr int STAGE = 9;
+  uint4 k_half;
+  Decode k_dec, v_dec;
+  int kref_0 = 0, kref_1 = 0;  // largest key exponents of tiles j + 1 and j
+  auto stage_begin = [&]() {
+    ek_0 = __builtin_amdgcn_readfirstlane(ek_next);
+    ev_0 = __builtin_amdgcn_readfirstlane(ev_next);
+    kref_1 = kref_0;
+    kref_0 = largest_exponent(ek_0);
+    evr = max(evr, largest_exponent(ev_0));
+    k_dec = Decode((ek_0 >> (8 * c_group)) & 0xFF, kref_0);
+    const int e = (ev_0 >> (8 * c_group)) & 0xFF;
+    v_dec = Decode(e == 255 ? 0 : e, evr);  // (a poisoned page is told to the rows that see it)
+  };
+  auto stage_step = [&](int j, int step) {
+    if (step < 4) {
+      const uint2 x = k_dec(step == 0 ? kc.x : step == 1 ? kc.y : step == 2 ? kc.z : kc.w);
+      if (step & 1) {
+        k_half.z = x.x;
+        k_half.w = x.y;
+        *(uint4*)(lds_k[(j + 1) & 1] + k_dst + (step >> 1) * 512) = k_half;
+      } else {
+        k_half.x = x.x;
+        k_half.y = x.y;
       }
+    } else if (step < 8) {
+      *(uint2*)(lds_v[j & 1] + v_dst + (step - 4) * 128) =
+          v_dec(step == 4 ? vc.x : step == 5 ? vc.y : step == 6 ? vc.z : vc.w);
+    } else {
+      kc = *(const uint4*)(k_src + key_at);
+      vc = *(const uint4*)(v_src + value_at);
     }
   };
 
-  f32x16_t O[RB][2 * DB];
-  float m[RB], l[RB];
+  f32x16_t O[2 * DB], S[MT];
+  u32x4_t P[NG];
+  float m = kNegInf, l = 0.f;
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    m[rb] = kNegInf;
-    l[rb] = 0.f;
+  for (int o = 0; o < 2 * DB; ++o)
 #pragma unroll
-    for (int o = 0; o < 2 * DB; ++o)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) O[rb][o][e] = 0.f;
-  }
+    for (int e = 0; e < 16; ++e) O[o][e] = 0.f;
   int evo = 0;  // O is in units of 2^(evo - 127)
 
-  if (tiles > 0) {
-    fill_window(0);
-    __syncthreads();
-    load_codes(0);
-    decode(0);
-    if (tiles > 1) load_codes(1);
-    __syncthreads();
-  }
-  for (int j = 0; j < tiles; ++j) {
+  const uint8_t *kd = lds_k[0] + lane * 16, *vd = lds_v[0] + lane * 16;
+  // what the weights of tile j need, in the phase that has room for it
+  float c = 0.f;
+  int sink = 0;
+  int cold = 0;  // not 0: a mask, a scale to take out of O or a poisoned page
+  auto prepare = [&](int j) {
     const int32_t key0 = c0 + j * KT;
-    const int ekt = ek_tile, evt = evr;
-    const bool poisoned = v_bad;
-    const uint32_t ev_bytes = v_bytes;
-    if (key0 <= some_last && key0 + KT > some_first) {
-      const uint8_t* kd = lds[j & 1] + lane * 16;
-      const uint8_t* vd = kd + KB;
-      f32x16_t S[RB][MT];
+    // (held above 0: a masked -infinity stays one)
+    const float cs = scale_of(kref_1) * cq, tiny = __uint_as_float(1u << 23);
+    c = cs < tiny ? tiny : cs;
+    sink = evo - evr;  // <= 0
+    evo = evr;
+    // (a byte of 255 is the only one whose complement is 0)
+    cold = (int)(key0 + KT - 1 > all_last) | (int)(key0 < all_first) | sink |
+           (int)((~ev_0 - 0x01010101u) & ev_0 & 0x80808080u);
+    asm volatile("" : "+v"(c));
+  };
+  // Multiply (j): O += P V of tile j - 1 (not at j = 0), S = K Q of tile j, and stage (j).  The
+  // operands are read AHEAD products before their use into a ring of registers; every step
+  // stays where it is written.
+  constexpr int PV = NG * 2 * DB, QK = MT * KS;  // products
+  auto multiply = [&](int j, auto with_values) {
+    constexpr int FIRST = decltype(with_values)::value ? 0 : PV, AHEAD = DB == 4 ? 3 : 6;
+    const uint8_t *kp = kd + (j & 1) * KB, *vp = vd + ((j + 1) & 1) * KB;
+    auto operand = [&](int i) { return *(const u32x4_t*)(i < PV ? vp + i * 1024 : kp + (i - PV) * 1024); };
+    u32x4_t ring[AHEAD];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+    for (int i = 0; i < AHEAD; ++i) ring[i] = operand(FIRST + i);
+    stage_begin();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
+    for (int i = FIRST; i < PV + QK; ++i) {
+      const u32x4_t x = ring[(i - FIRST) % AHEAD];
+      if (i < PV) {
+        O[i % (2 * DB)] = mma32(x, P[i / (2 * DB)], O[i % (2 * DB)]);
+      } else {
+        const int mt = (i - PV) / KS, k = (i - PV) % KS;
+        f32x16_t zero;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) S[rb][mt][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const u32x4_t kf = *(const u32x4_t*)(kd + (mt * KS + k) * 1024);
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) S[rb][mt] = mma32(kf, q[rb][k], S[rb][mt]);
-        }
+        for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+        S[mt] = mma32(x, q[k], k == 0 ? zero : S[mt]);
       }
-      const bool mask = key0 + KT - 1 > all_last || key0 < all_first;
-      const int sink = evo - evt;  // <= 0
-      evo = evt;
-      const float o_shift = sink <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + sink) << 23);
-      u32x4_t P[RB][NG];
+      if (i + AHEAD < PV + QK) ring[(i - FIRST) % AHEAD] = operand(i + AHEAD);
+      const int at = i - FIRST;
+      if (FIRST) {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        // (held above 0: a masked -infinity stays one)
-        const float c0 = scale_of(ekt) * cq[rb], tiny = __uint_as_float(1u << 23), c = c0 < tiny ? tiny : c0;
-        if (mask) {
-          // key - (key0 + 4 h) lies in lo .. hi for the row's keys
-          const int32_t at = opaque(key0 + 4 * h), lo = first[rb] - at, hi = last[rb] - at;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int32_t k = 32 * mt + 8 * (e >> 2) + (e & 3);
-              if (k > hi || k < lo) S[rb][mt][e] = kNegInf;
-            }
-        }
-        float mx = kNegInf;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) mx = max3(mx, S[rb][mt][e], S[rb][mt][e + 1]);
-        mx = fmaxf(max_over_halves(mx) * c, m[rb]);
-        if (__builtin_amdgcn_ballot_w64(mx > m[rb]) != 0 || sink != 0) {
-          const float al = mx > m[rb] ? __builtin_amdgcn_exp2f(m[rb] - mx) : 1.f;
-          l[rb] *= al;
-          const float f = al * o_shift;
-#pragma unroll
-          for (int o = 0; o < 2 * DB; ++o)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) O[rb][o][e] *= f;
-          m[rb] = mx;
-        }
-        const float bias = kWeightBits - (m[rb] == kNegInf ? 0.f : m[rb]);
-        float sum = 0.f;
+        for (int st = 0; st < (at == 0 ? STAGE : 0); ++st) stage_step(j, st);
+      } else if (at < STAGE) {
+        stage_step(j, at);
+      }
+      if (at == (FIRST ? 0 : STAGE + 2)) prepare(j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto weigh = [&](int j) {  // P from S
+    if (__builtin_expect(cold != 0, 0)) {
+      const int32_t key0 = c0 + j * KT;
+      if (key0 + KT - 1 > all_last || key0 < all_first) {
+        // key - (key0 + 4 h) lies in lo .. hi for the row's keys
+        const int32_t at = opaque(key0 + 4 * h), lo = first - at, hi = last - at;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            S[rb][mt][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[rb][mt][e], c, bias));
-            sum += S[rb][mt][e];
+            const int32_t k = 32 * mt + 8 * (e >> 2) + (e & 3);
+            if (k > hi || k < lo) S[mt][e] = kNegInf;
           }
-        l[rb] += sum;
-        if (poisoned) {  // a row that sees a key of a poisoned value page is NaN
-          const int32_t at = opaque(key0);
-          for (int g = 0; g < NG; ++g)
-            if (((ev_bytes >> (8 * g)) & 0xFF) == 0xFF && first[rb] < at + 16 * (g + 1) && last[rb] >= at + 16 * g)
-              l[rb] = __builtin_nanf("");
-        }
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int j2 = 0; j2 < 4; ++j2)
-            P[rb][g][j2] = pack_f16x2(S[rb][g >> 1][8 * (g & 1) + 2 * j2], S[rb][g >> 1][8 * (g & 1) + 2 * j2 + 1]);
       }
-#pragma unroll
       for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int o = 0; o < 2 * DB; ++o) {
-          const u32x4_t vf = *(const u32x4_t*)(vd + (g * 2 * DB + o) * 1024);
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) O[rb][o] = mma32(vf, P[rb][g], O[rb][o]);
+        if (((ev_0 >> (8 * g)) & 0xFF) == 0xFF) {  // a row that sees a key of a poisoned value page is NaN
+          const int32_t at = opaque(key0 + 16 * g);
+          if (first < at + 16 && last >= at) l = __builtin_nanf("");
         }
-    }
-    if (j + 1 < tiles) {
-      decode((j + 1) & 1);
-      if (j + 2 < tiles) {
-        if ((j + 2) % WIN == 0) {
-          __syncthreads();
-          fill_window(j + 2);
-          __syncthreads();
-        }
-        load_codes(j + 2);
+      if (sink != 0) {
+        const float f = sink <= -127 ? 0.f : __uint_as_float((uint32_t)(127 + sink) << 23);
+#pragma unroll
+        for (int o = 0; o < 2 * DB; ++o)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) O[o][e] *= f;
       }
     }
+    float mx = kNegInf;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) mx = max3(mx, S[mt][e], S[mt][e + 1]);
+    mx = fmaxf(max_over_halves(mx) * c, m);
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(mx > m) != 0, 0)) {
+      const float f = mx > m ? __builtin_amdgcn_exp2f(m - mx) : 1.f;
+      l *= f;
+#pragma unroll
+      for (int o = 0; o < 2 * DB; ++o)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) O[o][e] *= f;
+      m = mx;
+    }
+    const float bias = kWeightBits - (m == kNegInf ? 0.f : m);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        S[mt][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[mt][e], c, bias));
+        sum[e & 3] += S[mt][e];
+      }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    asm volatile("" : "+v"(l));  // (here, not between the products, where it would hold 32 registers)
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int j2 = 0; j2 < 4; ++j2)
+        P[g][j2] = pack_f16x2(S[g >> 1][8 * (g & 1) + 2 * j2], S[g >> 1][8 * (g & 1) + 2 * j2 + 1]);
+  };
+
+  if (tiles > 0) {
     __syncthreads();
+    find_keys(0);
+    find_values(0);
+    kc = *(const uint4*)(k_src + key_at);
+    vc = *(const uint4*)(v_src + value_at);
+    ek_next = exponents(win_ek, 0);
+    stage_begin();
+#pragma unroll
+    for (int step = 0; step < 4; ++step) stage_step(-1, step);  // the keys of tile 0
+    evr = 0;
+    find_keys(1);
+    kc = *(const uint4*)(k_src + key_at);
+    ask(0);
+    __syncthreads();
+    if (late) __syncthreads();
+    multiply(0, std::false_type{});
+    __syncthreads();
+    for (int j = 0; j < tiles; ++j) {
+      ask(j + 1);
+      weigh(j);
+      __syncthreads();
+      multiply(j + 1, std::true_type{});  // (after the last tile its scores are not used)
+      // half a window behind its use, the ring's older half is filled anew
+      if (__builtin_expect(j % WIN == WIN / 2 && j > WIN, 0)) fill_window((j / WIN + 1) * WIN, WIN);
+      __syncthreads();
+    }
+    if (!late) __syncthreads();  // evens the halves out
   }
 
   // ---- outputs: 16 consecutive columns per lane and 32-column block
   const bool direct = chunks == 1;
   const int64_t q_heads = (int64_t)a.c.heads * a.group, all_rows = a.c.tokens * q_heads;
   const float unit = scale_of(evo);
+  const float lg = sum_over_halves(l);
+  const float share = lg == 0.f ? 0.f : 1.f / lg;
+  if (!live) return;
+  const int i = row / a.group, qh = hk * a.group + row - i * a.group;
+  const int64_t at = (t.row + i) * q_heads + qh;
+  if (h == 0) {
+    const float lse2 = lg == 0.f ? kNegInf : m + __builtin_log2f(lg) - kWeightBits;
+    if (!direct) a.part_l[split * all_rows + at] = lse2;
+    else if (a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
+  }
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    const float lg = sum_over_halves(l[rb]);
-    const float share = lg == 0.f ? 0.f : 1.f / lg;
-    const int row = wr0 + 32 * rb + r;
-    if (row >= t.r1) continue;
-    const int i = row / a.group, qh = hk * a.group + row % a.group;
-    const int64_t at = (t.row + i) * q_heads + qh;
-    if (h == 0) {
-      const float lse2 = lg == 0.f ? kNegInf : m[rb] + __builtin_log2f(lg) - kWeightBits;
-      if (!direct) a.part_l[split * all_rows + at] = lse2;
-      else if (a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
-    }
+  for (int o = 0; o < 2 * DB; ++o) {
+    const int d = 32 * o + 16 * h;  // element 4 a + b of the accumulator is column d + 4 b + a
+    float v[16];
 #pragma unroll
-    for (int o = 0; o < 2 * DB; ++o) {
-      const int d = 32 * o + 16 * h;  // element 4 a + b of the accumulator is column d + 4 b + a
-      float v[16];
+    for (int e = 0; e < 16; ++e) v[4 * (e & 3) + (e >> 2)] = O[o][e] * share * unit;
+    if (direct) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[4 * (e & 3) + (e >> 2)] = O[rb][o][e] * share * unit;
-      if (direct) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float x[8] = {v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3],
-                              v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
-          store_out8(a, t.row + i, qh, d + 8 * k, x);
-        }
-      } else {
-        float* po = a.part_o + (split * all_rows + at) * (64 * DB) + d;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) *(float4*)(po + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      for (int k = 0; k < 2; ++k) {
+        const float x[8] = {v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3],
+                            v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
+        store_out8(a, t.row + i, qh, d + 8 * k, x);
       }
+    } else {
+      float* po = a.part_o + (split * all_rows + at) * (64 * DB) + d;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *(float4*)(po + 4 * k) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     }
   }
 }
@@ -1045,15 +1066,13 @@ constexpr int64_t kTileCost = 192;
 
 // More rows than this take the tile kernel.
 constexpr int kRowKernelRows = 64;
-constexpr int kTileWaves = 8;
-int tile_row_blocks(const AttnArgs&) { return 1; }
 
 }  // namespace
 
 int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
   const int64_t all = (int64_t)a->c.max_tokens * a->group;
   const bool tiled = all > kRowKernelRows;
-  a->tile_rows = tiled ? 32 * tile_row_blocks(*a) * kTileWaves : 16 * row_blocks(*a);
+  a->tile_rows = tiled ? 32 * kTileWaves : 16 * row_blocks(*a);
   a->tiles = (int32_t)((all + a->tile_rows - 1) / a->tile_rows);
   a->shares = 0;
   a->chunk = INT32_MAX / 2;
@@ -1102,10 +1121,10 @@ wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
     const unsigned blocks = (unsigned)(spread ? (items + 7) / 8 * 8 : (int64_t)(pairs + 7) / 8 * 8 * a.tiles);
     auto go = [&](auto kernel) { kernel<<<blocks, 64 * kTileWaves, 0, s>>>(a, pairs, spread); };
     switch (a.c.blocks) {
-      case 1: go(attn_tile_kernel<1, 1, kTileWaves, 64>); break;
-      case 2: go(attn_tile_kernel<2, 1, kTileWaves, 64>); break;
-      case 3: go(attn_tile_kernel<3, 1, kTileWaves, 32>); break;
-      case 4: go(attn_tile_kernel<4, 1, kTileWaves, 32>); break;
+      case 1: go(attn_tile_kernel<1, 64>); break;
+      case 2: go(attn_tile_kernel<2, 64>); break;
+      case 3: go(attn_tile_kernel<3, 32>); break;
+      case 4: go(attn_tile_kernel<4, 32>); break;
       default: return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: no kernel for this head_dim");
     }
   } else {
