@@ -609,7 +609,7 @@ __device__ __forceinline__ float sum_over_halves(float v) {
 constexpr int kTileWaves = 8;
 
 template <int DB, int KT>
-__global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs a, uint32_t pairs,
+__global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_kernel(AttnArgs a, uint32_t pairs,
                                                                                      bool spread) {
   constexpr int MT = KT / 32, NG = KT / 16;  // 32-key blocks and 16-key groups of a tile
   constexpr int KS = 4 * DB;                 // 16-column steps of a row
@@ -678,7 +678,6 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
     const uint8_t* p = win + NG * (j % (2 * WIN));
     return NG == 4 ? *(const uint32_t*)p : (uint32_t) * (const uint16_t*)p;
   };
-  if (tiles > 0) fill_window(0, 2 * WIN);
 
   // ---- this wave's rows
   const int wr0 = t.r0 + 32 * wave, wr1 = min(wr0 + 32, t.r1), row = wr0 + r;
@@ -696,6 +695,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
       raw[k] = make_uint4(0, 0, 0, 0);
       if (live && d < a.c.dim) raw[k] = *(const uint4*)(src + d);
     }
+    if (tiles > 0) fill_window(0, 2 * WIN);
     // lanes l and l ^ 32 share a row
     cq = query_operands(a, raw, q, [](uint32_t v) { return (uint32_t)max_over_halves((float)v); });
     last = live ? last_key(a, t, i) : -1;
@@ -799,8 +799,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
   // operands are read AHEAD products before their use into a ring of registers; every step
   // stays where it is written.
   constexpr int PV = NG * 2 * DB, QK = MT * KS;  // products
+  constexpr int PACE = PV + QK < STAGE + 3 ? 2 : 1;  // steps of staging per product
+  static_assert((STAGE + 2) / PACE < PV + QK, "the staging fits between the products");
   auto multiply = [&](int j, auto with_values) {
-    constexpr int FIRST = decltype(with_values)::value ? 0 : PV, AHEAD = DB == 4 ? 3 : 6;
+    constexpr int FIRST = decltype(with_values)::value ? 0 : PV, AHEAD = DB == 2 || DB == 3 ? 6 : 3;
     const uint8_t *kp = kd + (j & 1) * KB, *vp = vd + ((j + 1) & 1) * KB;
     auto operand = [&](int i) { return *(const u32x4_t*)(i < PV ? vp + i * 1024 : kp + (i - PV) * 1024); };
     u32x4_t ring[AHEAD];
@@ -825,10 +827,11 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
       if (FIRST) {
 #pragma unroll
         for (int st = 0; st < (at == 0 ? STAGE : 0); ++st) stage_step(j, st);
-      } else if (at < STAGE) {
-        stage_step(j, at);
+      } else {
+#pragma unroll
+        for (int st = at * PACE; st < min((at + 1) * PACE, STAGE); ++st) stage_step(j, st);
       }
-      if (at == (FIRST ? 0 : STAGE + 2)) prepare(j);
+      if (at == (FIRST ? 0 : (STAGE + 2) / PACE)) prepare(j);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -859,11 +862,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
           for (int e = 0; e < 16; ++e) O[o][e] *= f;
       }
     }
-    float mx = kNegInf;
+    float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) mx = max3(mx, S[mt][e], S[mt][e + 1]);
+      for (int e = 0; e < 16; e += 2) mq[(e >> 1) & 3] = max3(mq[(e >> 1) & 3], S[mt][e], S[mt][e + 1]);
+    float mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]);
     mx = fmaxf(max_over_halves(mx) * c, m);
     if (__builtin_expect(__builtin_amdgcn_ballot_w64(mx > m) != 0, 0)) {
       const float f = mx > m ? __builtin_amdgcn_exp2f(m - mx) : 1.f;
@@ -914,7 +918,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
       ask(j + 1);
       weigh(j);
       __syncthreads();
-      multiply(j + 1, std::true_type{});  // (after the last tile its scores are not used)
+      __builtin_amdgcn_s_setprio(2);  // a product that is ready goes first: the matrix cores are what is waited for
+      multiply(j + 1, std::true_type{});
+      __builtin_amdgcn_s_setprio(0);  // (after the last tile its scores are not used)
       // half a window behind its use, the ring's older half is filled anew
       if (__builtin_expect(j % WIN == WIN / 2 && j > WIN, 0)) fill_window((j / WIN + 1) * WIN, WIN);
       __syncthreads();
@@ -1062,7 +1068,7 @@ int row_blocks(const AttnArgs& a) {
 // workgroups of the row kernel that a CU holds (its registers decide)
 int rows_per_cu(int blocks, int nb) { return blocks * nb <= 2 ? 3 : blocks * nb <= 4 ? 2 : 1; }
 
-constexpr int64_t kTileCost = 192;
+constexpr int64_t kTileCost = 1000;
 
 // More rows than this take the tile kernel.
 constexpr int kRowKernelRows = 64;
@@ -1095,13 +1101,16 @@ int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
     a->shares = (int32_t)shares;
     return room;
   }
-  // The split whose rounds of workgroups over the CUs take least: a round costs its keys and
-  // kTileCost keys' worth of queries and outputs (with partial results, twice that).
+  // The split whose rounds of workgroups over the CUs take least, in keys: a round takes its keys
+  // and kTileCost / blocks for queries and outputs; the partial results of a split are
+  // written and read, 8 D64 bytes a row, while the matrix cores take some 0.015 us a key and
+  // 64-column block: rows / 128 keys.
   const int64_t rows = a->c.tokens * (int64_t)a->c.heads * a->group, cus = device_cus();
-  int64_t best = 1, best_cost = (items + cus - 1) / cus * (span + kTileCost);
-  for (int64_t n = 2; n <= 16 && rows * n <= most; ++n) {
-    const int64_t chunk = (span + n - 1) / n, cost = (items * n + cus - 1) / cus * (chunk + 2 * kTileCost);
-    if (chunk >= 256 && cost < best_cost) {
+  int64_t best = 1, best_cost = 0;
+  for (int64_t n = 1; n <= 16 && (n == 1 || rows * n <= most); ++n) {
+    const int64_t chunk = (span + n - 1) / n;
+    const int64_t cost = (items * n + cus - 1) / cus * (chunk + kTileCost / a->c.blocks) + (n > 1 ? n * rows / 128 : 0);
+    if (n == 1 || (chunk >= 256 && cost < best_cost)) {
       best = n;
       best_cost = cost;
     }
