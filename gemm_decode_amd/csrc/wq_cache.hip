@@ -37,15 +37,21 @@ __device__ __forceinline__ uint32_t exponent_byte(uint32_t bits) {
 // 2^(127 - b) for an exponent byte b in 1 .. 253
 __device__ __forceinline__ float inverse_scale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
-// codes are stored as q + 128; |x * inv| <= 127 by the choice of the exponent
-__device__ __forceinline__ uint32_t code_of(float x, float inv) { return (uint32_t)((int)__builtin_rintf(x * inv) + 128); }
+// Codes are stored as q + 128.  With |x * inv| <= 127 (by the choice of the exponent; the
+// product with a power of two is exact) the fma's rounding to nearest even at 1.5 * 2^23 is
+// that of rint, and the sum's low byte is the code.
+constexpr float kCodeBase = 12582912.f + 128.f;
+__device__ __forceinline__ uint32_t code_bits(float x, float inv) { return __float_as_uint(__builtin_fmaf(x, inv, kCodeBase)); }
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {  // a | b << 8 | ...
+  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0C0C0400u), cd = __builtin_amdgcn_perm(d, c, 0x0C0C0400u);
+  return __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+}
 // four older codes of a word under a scale that grew by 2^d (shrink = 2^-d, 0 when nothing is left)
 __device__ __forceinline__ uint32_t shrink_word(uint32_t w, float shrink) {
-  uint32_t o = 0;
+  uint32_t c[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    o |= (uint32_t)((int)__builtin_rintf((float)((int)((w >> (8 * j)) & 0xFFu) - 128) * shrink) + 128) << (8 * j);
-  return o;
+  for (int j = 0; j < 4; ++j) c[j] = code_bits((float)((w >> (8 * j)) & 0xFFu) - 128.f, shrink);
+  return low_bytes(c[0], c[1], c[2], c[3]);
 }
 
 // largest value of a wave, in every lane
@@ -123,13 +129,30 @@ __global__ __launch_bounds__(WPP > 4 ? 64 * WPP : 256) void kv_write_kernel(KvAr
 #pragma unroll
   for (int k = 0; k < NG; ++k)
 #pragma unroll
-    for (int b = 0; b < DB; ++b)
+    for (int b = 0; b < DB; ++b) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int slot = 16 * (group0 + k) + (values ? 4 * g + e : i), d = 64 * b + (values ? 4 * i : 16 * g + 4 * e);
-        w[k][b][e] = make_uint2(0, 0);
-        if (slot >= lo && slot < hi && d < a.dim) w[k][b][e] = *(const uint2*)(x + (int64_t)(slot - lo) * src.ts + d);
+      for (int e = 0; e < 4; ++e) w[k][b][e] = make_uint2(0, 0);
+      if (values) {
+        const int d = 64 * b + 4 * i;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int slot = 16 * (group0 + k) + 4 * g + e;
+          if (slot >= lo && slot < hi && d < a.dim) w[k][b][e] = *(const uint2*)(x + (int64_t)(slot - lo) * src.ts + d);
+        }
+      } else {
+        const int slot = 16 * (group0 + k) + i, d = 64 * b + 16 * g;
+        if (slot >= lo && slot < hi) {
+          const uint16_t* row = x + (int64_t)(slot - lo) * src.ts + d;
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            if (d + 8 * v < a.dim) {
+              const uint4 q4 = *(const uint4*)(row + 8 * v);
+              w[k][b][2 * v] = make_uint2(q4.x, q4.y);
+              w[k][b][2 * v + 1] = make_uint2(q4.z, q4.w);
+            }
+        }
       }
+    }
   const bool in_pool = (uint32_t)page < (uint64_t)a.pages;
   const int64_t ph = (int64_t)(in_pool ? page : 0) * a.heads + h;
   uint8_t* ep = (values ? a.ve : a.ke) + ph;
@@ -200,20 +223,23 @@ __global__ __launch_bounds__(WPP > 4 ? 64 * WPP : 256) void kv_write_kernel(KvAr
         const uint2 v = w[k][cb][e];
         const uint32_t el[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[e][j] = poison ? 0x80u : code_of(to_f32<F16>(el[j]), inv);
+        for (int j = 0; j < 4; ++j) c[e][j] = code_bits(to_f32<F16>(el[j]), inv);
       }
       uint32_t word[4];
       if (!values) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) word[e] = c[e][0] | c[e][1] << 8 | c[e][2] << 16 | c[e][3] << 24;
+        for (int e = 0; e < 4; ++e) word[e] = low_bytes(c[e][0], c[e][1], c[e][2], c[e][3]);
       } else {
         uint4 o = old[cb];
         if (grow && merge) o = shrink_chunk(o);
         const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          word[j] = (ow[j] & keep) | ((c[0][j] | c[1][j] << 8 | c[2][j] << 16 | c[3][j] << 24) & ~keep);
+          word[j] = (ow[j] & keep) | (low_bytes(c[0][j], c[1][j], c[2][j], c[3][j]) & ~keep);
       }
+      if (poison)  // (what is no number has no code)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) word[j] = 0x80808080u;
       *chunk(group, cb) = make_uint4(word[0], word[1], word[2], word[3]);
     }
   }
@@ -223,18 +249,21 @@ __global__ __launch_bounds__(WPP > 4 ? 64 * WPP : 256) void kv_write_kernel(KvAr
       for (int c = 0; c < DB; ++c) *chunk(group, c) = shrink_chunk(*chunk(group, c));
 }
 
+// two values of codes (bytes j0 and j1 of w0 and w1) as 16-bit numbers: the products are exact
+// in fp32 (or overflow to an infinity, which the clamp takes back with all beyond the type)
 template <bool F16>
-__device__ __forceinline__ uint32_t value_bits(uint32_t code, float scale) {
-  // the product is exact in fp32 (or overflows to an infinity, which the clamp takes back)
-  const float v = (float)((int)code - 128) * scale;
+__device__ __forceinline__ uint32_t value_pair(uint32_t c0, uint32_t c1, float scale) {
   const float top = F16 ? 65504.f : __uint_as_float(0x7F7F0000u);
-  const float w = v > top ? top : v < -top ? -top : v;  // (a NaN stays one)
-  return F16 ? __builtin_bit_cast(uint16_t, (_Float16)w) : __builtin_bit_cast(uint16_t, (__bf16)w);
+  const float v0 = __builtin_amdgcn_fmed3f(((float)c0 - 128.f) * scale, -top, top);
+  const float v1 = __builtin_amdgcn_fmed3f(((float)c1 - 128.f) * scale, -top, top);
+  if constexpr (F16) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, h2{(_Float16)v0, (_Float16)v1});
+  } else {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, b2{(__bf16)v0, (__bf16)v1});
+  }
 }
-__device__ __forceinline__ float scale_of(uint32_t b) {
-  return b == 255u ? __builtin_nanf("") : __uint_as_float(b << 23);
-}
-
 // one wave per (sequence, 16-token group, head, 64-column block), the last fastest
 template <bool F16>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, KvTokens kt, KvTokens vt, int span, int waves) {
@@ -254,7 +283,9 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, KvTokens kt, KvT
   const int64_t off = ((ph << a.tshift) + (g0 & ((1 << a.tshift) - 1))) * (64 * a.blocks) + blk * 1024 + lane * 16;
   const uint4 kw = *(const uint4*)(a.kc + off), vw = *(const uint4*)(a.vc + off);
   const uint32_t kb = a.ke[ph], vb = a.ve[ph];
-  const float ks = scale_of(in_pool ? kb : 255u), vs = scale_of(in_pool ? vb : 255u);
+  const float ks = __uint_as_float(kb << 23), vs = __uint_as_float(vb << 23);
+  // a poisoned page, or one outside the pool, reads as NaN
+  const bool k_bad = !in_pool || kb == 255u, v_bad = !in_pool || vb == 255u;
   {  // keys: 16 columns of token lane % 16
     const int64_t pos = g0 + (lane & 15);
     const int d = 64 * blk + 16 * (lane >> 4);
@@ -268,7 +299,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, KvTokens kt, KvT
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t w = ww[2 * v + (j >> 1)] >> (16 * (j & 1));
-            o[j] = value_bits<F16>(w & 0xFFu, ks) | value_bits<F16>((w >> 8) & 0xFFu, ks) << 16;
+            o[j] = k_bad ? 0x7FFF7FFFu : value_pair<F16>(w & 0xFFu, (w >> 8) & 0xFFu, ks);
           }
           *(uint4*)(y + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -285,8 +316,8 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, KvTokens kt, KvT
         uint32_t o[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          o[j] = value_bits<F16>((ww[2 * j] >> (8 * e)) & 0xFFu, vs) |
-                 value_bits<F16>((ww[2 * j + 1] >> (8 * e)) & 0xFFu, vs) << 16;
+          o[j] = v_bad ? 0x7FFF7FFFu
+                       : value_pair<F16>((ww[2 * j] >> (8 * e)) & 0xFFu, (ww[2 * j + 1] >> (8 * e)) & 0xFFu, vs);
         *(uint2*)y = make_uint2(o[0], o[1]);
       }
     }
