@@ -94,15 +94,18 @@ __device__ __forceinline__ int32_t steps_of(const Tile& t) { return max((t.hi - 
 // --- equal shares of the row kernel ---
 // The items (sequence and row tile, key/value head) lie one after another on a line, in that
 // order: an item is kItemCost units for what it costs whatever its length (queries, joining
-// the waves), then its steps of 32 keys.  Workgroup w of `shares` takes units w * share ..
+// the waves; 64 sequences of up to 8191 keys, 28 over 4 heads of 192, 8 tokens each: 230 us with
+// 8, 178 with 24, 182 with 48; 32 over 8 heads of 128, one token: 97, 98 and 102), then its
+// steps of 32 keys.  Workgroup w of `shares` takes units w * share ..
 // of the line, whatever items they belong to, so sequences of any lengths load the CUs
 // alike.  Every workgroup forms the line itself (a scan over the sequences' lengths, in
 // LDS); workgroup 0 leaves it in memory for the join.  A workgroup cuts at most two items:
 // the one it starts inside of (its partial results go to slot 2 w) and the one it leaves
 // unfinished (slot 2 w + 1).  Line positions stay below 2^31 (plan_attention sees to it).
 constexpr int kLineMax = 1024;  // sequences x row tiles that the scan takes
-constexpr int kMinShare = 4;    // steps: one per wave
-constexpr int kItemCost = 8;
+constexpr int kMinShare = 4;    // steps: one per wave (one sequence of 2582 keys, 24 over 4 heads of 256: 17.0 us,
+                                // with 8 18.0, with 16 22.1)
+constexpr int kItemCost = 20;
 
 // line[i]: units of one head before sequence and tile i, 0 <= i <= seqs x tiles; 256 threads
 __device__ __forceinline__ void scan_line(const AttnArgs& a, int32_t* line) {
@@ -374,7 +377,7 @@ __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, in
         float sc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sc[e] = S[nb][e >> 2][e & 3] * (kf[e >> 2] * cq[nb]);
-        if (mask) {
+        if (__builtin_expect(mask, 0)) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int32_t key = key0 + 16 * (e >> 2) + 4 * g + (e & 3);
@@ -383,7 +386,7 @@ __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, in
         }
         float mx = max3(max3(sc[0], sc[1], sc[2]), max3(sc[3], sc[4], sc[5]), fmaxf(sc[6], sc[7]));
         mx = fmaxf(max_over_groups(mx), m[nb]);
-        if (__builtin_amdgcn_ballot_w64(mx > m[nb]) != 0 || sink != 0) {
+        if (__builtin_expect(__builtin_amdgcn_ballot_w64(mx > m[nb]) != 0 || sink != 0, 0)) {
           const float al = mx > m[nb] ? __builtin_amdgcn_exp2f(m[nb] - mx) : 1.f;
           l[nb] *= al;
           const float f = al * o_shift;
@@ -495,7 +498,7 @@ __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, in
 }
 
 template <int DB, int NB>
-__global__ __launch_bounds__(64 * kWaves, DB * NB <= 4 ? 2 : 1) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, DB * NB <= 2 ? 3 : DB * NB <= 4 ? 2 : 1) void attn_rows_kernel(AttnArgs a) {
   __shared__ int32_t line[kLineMax + 1];
   Tile t;
   if (a.shares == 0) {  // an item each
@@ -802,7 +805,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
   constexpr int PACE = PV + QK < STAGE + 3 ? 2 : 1;  // steps of staging per product
   static_assert((STAGE + 2) / PACE < PV + QK, "the staging fits between the products");
   auto multiply = [&](int j, auto with_values) {
-    constexpr int FIRST = decltype(with_values)::value ? 0 : PV, AHEAD = DB == 2 || DB == 3 ? 6 : 3;
+    constexpr int FIRST = decltype(with_values)::value ? 0 : PV, AHEAD = 3;
     const uint8_t *kp = kd + (j & 1) * KB, *vp = vd + ((j + 1) & 1) * KB;
     auto operand = [&](int i) { return *(const u32x4_t*)(i < PV ? vp + i * 1024 : kp + (i - PV) * 1024); };
     u32x4_t ring[AHEAD];
@@ -1065,12 +1068,27 @@ int row_blocks(const AttnArgs& a) {
   return nb;
 }
 
-// workgroups of the row kernel that a CU holds (its registers decide)
+// workgroups of the row kernel that a CU holds (its registers decide; three where four would
+// go, which measured the same)
 int rows_per_cu(int blocks, int nb) { return blocks * nb <= 2 ? 3 : blocks * nb <= 4 ? 2 : 1; }
 
-constexpr int64_t kTileCost = 1000;
+// Whether the row kernel's workgroups take an item each instead of equal shares: the shares
+// cost the scan, more pieces and the join (together some 8 us), an item of its own the time of
+// the longest one, some 3.5 + blocks ns a key, of which other items hide the more the more
+// there are.  Measured, shares against items: up to 1024 keys for 8, 512 sequences and heads of
+// 128, lengths anywhere: 13.3 / 10.6, 26 / 17 us; 4096 keys: 13.5 / 12.4 .. 31, 61 / 52 us; 8191
+// keys and 64, 512: 26 / 43, 101 / 111 us.
+bool items_alone(int64_t items, int64_t span, int blocks, int64_t cus) {
+  return span * (7 + 2 * blocks) * cus <= 16000 * (cus + std::min(items, 2 * cus));
+}
 
-// More rows than this take the tile kernel.
+// (4096-token prompt, 24 over 4 heads of 256: 380 us with 1000, in two splits, 314 with 3000, in one;
+// 1024 tokens behind 7168: 303 us with 250, 253 with 1000 and 3000, 408 without a split)
+constexpr int64_t kTileCost = 3000;
+
+// More rows than this take the tile kernel: 64 rows, 32 sequences of 4000 keys, 8 heads of 128:
+// 100 us in the row kernel, 122 in the tile kernel; 80 rows: 178 and 121; one sequence: 30 and
+// 26, 31 and 27.
 constexpr int kRowKernelRows = 64;
 
 }  // namespace
@@ -1090,12 +1108,13 @@ int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
   const int64_t items = (int64_t)a->c.seqs * a->c.heads * a->tiles;
   const int64_t most = (int64_t)(ws_bytes / ((64 * a->c.blocks + 1) * sizeof(float)));
   if (!tiled) {
-    // as many workgroups as the CUs hold at once, none with less than a step per wave
+    // as many workgroups as the CUs hold at once, none with less than a step per wave (in 64
+    // sequences of up to 8191 keys, 16 heads of 64: 60 us; with one workgroup per CU 100)
     const int64_t steps = items * (span / kStep);
     const int64_t shares = std::min<int64_t>(rows_per_cu(a->c.blocks, a->tile_rows / 16) * device_cus(),
                                              (steps + kMinShare - 1) / kMinShare);
     const int64_t room = 2 * shares * a->tile_rows + (kLineMax / (64 * a->c.blocks) + 64) / 64 * 64;  // and the line
-    if ((int64_t)a->c.seqs * a->tiles > kLineMax || span <= kMinShare * kStep || room > most ||
+    if ((int64_t)a->c.seqs * a->tiles > kLineMax || items_alone(items, span, a->c.blocks, device_cus()) || room > most ||
         items * (span / kStep + kItemCost) >= INT32_MAX)
       return 0;
     a->shares = (int32_t)shares;
@@ -1126,6 +1145,8 @@ wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
   if (items > INT32_MAX - 8 * (__int128)a.tiles) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
   if ((int64_t)a.c.max_tokens * a.group > kRowKernelRows) {
     const uint32_t pairs = (uint32_t)(items / a.tiles);
+    // 12 pairs of 4000 rows: 307 us spread, 381 not; 4 pairs of 28672: 289 and 401; 192 pairs of
+    // 2581 rows: 363 and 335; 8 pairs: 157 and 160
     const bool spread = pairs % 8 != 0 && pairs < 64;
     const unsigned blocks = (unsigned)(spread ? (items + 7) / 8 * 8 : (int64_t)(pairs + 7) / 8 * 8 * a.tiles);
     auto go = [&](auto kernel) { kernel<<<blocks, 64 * kTileWaves, 0, s>>>(a, pairs, spread); };
@@ -1156,12 +1177,14 @@ wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
   }
   WQ_HIP_CHECK(hipGetLastError());
   if (a.splits > 1 || a.shares > 0) {
-    // lanes for the pieces that a row has on average
+    // lanes for the pieces that a row has on average, as far as the CUs are idle (40 sequences, 4480
+    // rows: 28.4 us for the attention with one lane, 34.0 with 8; 24 rows of 20 pieces: 18 and 17)
     const int64_t rows = (int64_t)a.c.seqs * a.c.heads * a.c.max_tokens * a.group;
     const int cols = 8 * a.c.blocks;
     int lanes = 1;
     const int64_t pieces = a.shares > 0 ? a.shares / (int64_t)items + 2 : a.splits;
-    while (2 * lanes * cols <= 256 && lanes < pieces) lanes *= 2;
+    while (2 * lanes * cols <= 256 && lanes < pieces && rows * (2 * lanes * cols) <= 256 * (int64_t)device_cus())
+      lanes *= 2;
     const int64_t per = 256 / (cols * lanes);
     if (rows > INT32_MAX - 256) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
     attn_join_kernel<<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a, lanes);
