@@ -263,11 +263,14 @@ def least_weight(V, q_heads):
 
 
 def attention_case(wqlib, act, T, heads, kv_heads, dim, lens, causal=True, window=0, ws=True, kv_lens=None, scale=None,
-                   seed=0, qmul=1.0, strided=False, lse=True, max_kv=None):
-    """lens: (kv, n) per sequence, the n queries standing at the end; checks out and lse."""
+                   seed=0, qmul=1.0, strided=False, lse=True, max_kv=None, wide=0):
+    """lens: (kv, n) per sequence, the n queries standing at the end; checks out and lse.  wide: the
+    page table's least width (what a sequence may hold, which decides how the work is shared out)."""
     rng = np.random.default_rng(seed)
     kvs, ns = [kv for kv, _ in lens], [n for _, n in lens]
     table, pages = tables(rng, kvs, T)
+    if wide > table.shape[1]:
+        table = np.pad(table, ((0, 0), (0, wide - table.shape[1])), constant_values=-1)
     cache, ref = wqlib.KVCache(pages, T, kv_heads, dim), OA.PagedCache(pages, T, kv_heads, dim)
     for t in (cache.k_codes, cache.v_codes, cache.k_exps, cache.v_exps):
         t.fill_(255)                                   # what no token was written to must not matter
@@ -289,7 +292,7 @@ def attention_case(wqlib, act, T, heads, kv_heads, dim, lens, causal=True, windo
     batch = wqlib.KVBatch(i32(table), i32([kv - n for kv, n in lens]), i32(qo), max(1, max(ns)))
     buf = wqlib.workspace(wqlib.wq_kv_attention_workspace_size(cache, batch, heads, int(qo[-1]))) if ws is True else ws
     wqlib.wq_kv_attention(cache, batch, q, out, scale, causal=causal, window=window, lse=sums, ws=buf,
-                          kv_lens=None if kv_lens is None else i32(kv_lens), max_kv=max(kvs) if max_kv is None else max_kv)
+                          kv_lens=None if kv_lens is None else i32(kv_lens), max_kv=(0 if wide else max(kvs)) if max_kv is None else max_kv)
     o = f64(out)
     for b, (kv, n) in enumerate(lens):
         K, V = ref.read(table[b], 0, kv)
@@ -353,6 +356,50 @@ def test_attention_rows_that_see_nothing(wqlib, n):
 def test_attention_split_and_unsplit_agree_with_the_definition(wqlib, kv, n):
     for ws in (True, None, torch.empty(1 << 18, dtype=torch.uint8, device=DEV)):
         attention_case(wqlib, "bf16", 64, 4, 1, 128, [(kv, n), (n + 1, n), (700, min(n, 700))], ws=ws, seed=n)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("heads,kv_heads,dim", HEADS)
+@pytest.mark.parametrize("n", [1, 5])
+def test_attention_equal_shares(wqlib, act, heads, kv_heads, dim, n):
+    """Sequences that may be long: equal shares of all the work, whatever the lengths turn out to
+    be, none and one among them; and one long sequence among empty ones."""
+    n = min(n, 64 * kv_heads // heads)
+    lens = [(0, 0), (n, n), (1, 0), (n + 1, n), (31 + n, 1), (32, 1), (33, 1), (700, n), (0, 0), (129, 1)]
+    attention_case(wqlib, act, 32, heads, kv_heads, dim, lens, wide=600, seed=dim + n)
+    attention_case(wqlib, act, 32, heads, kv_heads, dim, [(0, 0), (1500, n), (0, 0)], wide=600, seed=dim)
+
+
+@pytest.mark.parametrize("window", [0, 2500])
+def test_attention_equal_shares_of_rows_that_see_nothing(wqlib, window):
+    lens = [(2, 9), (0, 9), (8, 9), (3000, 9), (1, 1)]
+    out = attention_case(wqlib, "bf16", 64, 4, 2, 128, lens, kv_lens=[kv for kv, _ in lens], window=window, wide=200)
+    assert (out[:7] == 0).all() and (out[9:18] == 0).all()
+
+
+def test_attention_equal_shares_keep_a_poisoned_page_in_its_sequence(wqlib):
+    rng = np.random.default_rng(19)
+    T, heads, dim, kv, B = 32, 2, 128, 1000, 3
+    table, pages = tables(rng, [kv] * B, T)
+    table = np.pad(table, ((0, 0), (0, 200)), constant_values=-1)
+    k, v = (draw(rng, (B * kv, heads, dim), "bf16") for _ in "kv")
+    q = draw(rng, (B, 2 * heads, dim), "bf16")
+    outs = []
+    for bad in (False, True):
+        if bad:
+            k[kv + 500, 0, 3] = math.nan           # sequence 1, head 0
+            v[2 * kv + 10, 1, 4] = math.inf        # sequence 2, head 1
+        cache = wqlib.KVCache(pages, T, heads, dim)
+        wqlib.wq_kv_write(cache, wqlib.KVBatch(i32(table), i32([0] * B), None, kv), k, v)
+        batch = wqlib.KVBatch(i32(table), i32([kv - 1] * B), None, 1)
+        ws = wqlib.workspace(wqlib.wq_kv_attention_workspace_size(cache, batch, 2 * heads, B))
+        out, lse = torch.empty_like(q), torch.empty(B, 2 * heads, device=DEV)
+        wqlib.wq_kv_attention(cache, batch, q, out, 0.1, lse=lse, ws=ws)
+        outs.append(out)
+    assert torch.isfinite(outs[0]).all()
+    assert torch.isnan(outs[1][1, :2]).all() and torch.isnan(outs[1][2, 2:]).all()
+    outs[1][1, :2], outs[1][2, 2:] = outs[0][1, :2], outs[0][2, 2:]
+    assert torch.equal(outs[0], outs[1])
 
 
 @pytest.mark.parametrize("n", [1, 90])
