@@ -241,7 +241,11 @@ __device__ __forceinline__ void store_out8(const AttnArgs& a, int64_t tok, int q
 // (the cache's layout: every load is one contiguous KB of a wave); the next step's keys are
 // loaded once the scores have used the current ones, its values after the outputs, so a
 // wave has one of the two in flight at any time (a second register set for both measured
-// no faster and costs a wave per SIMD).
+// no faster and costs a wave per SIMD).  Memory bounds it where there are many keys: 64
+// sequences of up to 8191 tokens, 32 over 8 heads of 128, 493 MB: 93 us with the join, 5.3 TB/s;
+// 4 sequences of 65536 to 131071: 132 us, 5.8 TB/s.  Few keys are bound by the chain of lengths,
+// pages, exponents, codes and the joining of the waves and pieces, 11 + 5 us (one token behind
+// 2581, 24 over 4 heads of 256).
 // slot < 0: the run is the whole item and the output is written; else the partial slot.
 template <int DB, int NB>
 __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, int s, int hk, int step0, int step1,
@@ -537,7 +541,15 @@ __global__ __launch_bounds__(64 * kWaves, DB * NB <= 2 ? 3 : DB * NB <= 4 ? 2 : 
 // wave, and walks the keys in tiles of KT.  The waves decode a tile's codes together into
 // fp16 operands in LDS, once for all rows, the codes of the next tile in flight in
 // registers; every wave multiplies its own rows by the whole tile on
-// v_mfma_f32_32x32x16_f16.
+// v_mfma_f32_32x32x16_f16.  KT is 64 up to 2 blocks of columns (with 32: 8192-token prompt 696
+// us against 560) and 32 beyond, where a tile of 64 has more chunks than there are threads and
+// the scores no registers.
+//
+// Measured: 8192-token prompt, 32 over 8 heads of 128: 544 us, 1010 TFLOP/s (the products alone
+// 455 at a library product's rate); 1024 tokens behind 7168, 24 over 4 heads of 256: 246 us, 784
+// TFLOP/s; 12 prompts of up to 2581, 16 heads of 64: 184 us, 500 TFLOP/s.  The vector units
+// bound it at 64 columns (a weight costs the same, its products half of those at 128), products
+// and weights about alike at 128, operands and the joining of splits at 256.
 //
 // The matrix cores and the vector units take about the same time for a tile (D = 128, 64
 // keys and 32 rows: 32 products of 32 cycles; 32 weights per lane at some 28 cycles, and the
@@ -545,7 +557,7 @@ __global__ __launch_bounds__(64 * kWaves, DB * NB <= 2 ? 3 : DB * NB <= 4 ? 2 : 
 // while waves 0-3 multiply (O += P V of the tile before, S = Q K of this one), waves 4-7
 // form weights, and the other way round, with a barrier between the phases.
 // With all eight in step both units stood idle half of the time (8192-token prompt, 32 over
-// 8 heads of 128: 622 us against TILE_FIG).
+// 8 heads of 128: 622 us against 575).
 //   phase 2 j      waves 0-3: multiply (j)     waves 4-7: weights (j - 1)
 //   phase 2 j + 1  waves 0-3: weights (j)      waves 4-7: multiply (j)
 // A wave issues about one instruction in 5 cycles, whatever its kind, and a taken branch costs
@@ -799,8 +811,9 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
     asm volatile("" : "+v"(c));
   };
   // Multiply (j): O += P V of tile j - 1 (not at j = 0), S = K Q of tile j, and stage (j).  The
-  // operands are read AHEAD products before their use into a ring of registers; every step
-  // stays where it is written.
+  // operands are read AHEAD products before their use into a ring of registers (6 measured the
+  // same at 2 and 3 blocks; at 4 it no longer fits them: 398 us against 253 for 1024 tokens
+  // behind 7168); every step stays where it is written.
   constexpr int PV = NG * 2 * DB, QK = MT * KS;  // products
   constexpr int PACE = PV + QK < STAGE + 3 ? 2 : 1;  // steps of staging per product
   static_assert((STAGE + 2) / PACE < PV + QK, "the staging fits between the products");
@@ -969,7 +982,8 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
 // ------------------------------------------------------------- joining partial results
 // out = sum_p w_p O_p / sum_p w_p, w_p = 2^(lse_p - max), over the pieces p of a row's keys.
 // A row takes `lanes` x 8 D64 / 64 threads: 8 columns each, every lanes-th piece; the lanes'
-// sums meet in LDS.  A workgroup holds 256 threads' worth of rows.
+// sums meet in LDS.  A workgroup holds 256 threads' worth of rows.  Bound by its latency: 4 to 8
+// us (2048 rows of some 3 pieces, 128 rows of 26).
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int lanes) {
   __shared__ float buf[256][11];  // 8 columns, maximum, sum (odd stride: no bank conflicts)
   const int cols = 8 * a.c.blocks, per = cols * lanes, rows = 256 / per;  // rows of a workgroup

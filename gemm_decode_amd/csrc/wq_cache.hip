@@ -14,6 +14,12 @@
 //                    scale grows are rewritten in place.
 //   kv_read_kernel   one wave per 16 tokens and 64 columns of a head: a 1 KB block of each
 //                    side in, rows out.
+//
+// Memory bounds both where there is much to move: 6 prompts of up to 8192 tokens, 8 heads of 128,
+// fp16, pages of 16: write 31 us, read 24 us, 60 us one after the other (3.3 TB/s; a copy
+// reaches 5.2).  One token per sequence, 256 sequences: 6 and 14 us, the launches' and the
+// chain's (length, page, exponent, codes) latency; one sequence: 5 and 5 us.  Non-temporal
+// loads on either side measured within 2 %.
 #include "wq_internal.h"
 
 namespace wq {
@@ -249,8 +255,8 @@ __global__ __launch_bounds__(WPP > 4 ? 64 * WPP : 256) void kv_write_kernel(KvAr
       for (int c = 0; c < DB; ++c) *chunk(group, c) = shrink_chunk(*chunk(group, c));
 }
 
-// two values of codes (bytes j0 and j1 of w0 and w1) as 16-bit numbers: the products are exact
-// in fp32 (or overflow to an infinity, which the clamp takes back with all beyond the type)
+// the values of two codes as 16-bit numbers: the products are exact in fp32 (or overflow to an
+// infinity, which the clamp takes back with all beyond the type)
 template <bool F16>
 __device__ __forceinline__ uint32_t value_pair(uint32_t c0, uint32_t c1, float scale) {
   const float top = F16 ? 65504.f : __uint_as_float(0x7F7F0000u);
@@ -264,6 +270,7 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t c0, uint32_t c1, float s
     return __builtin_bit_cast(uint32_t, b2{(__bf16)v0, (__bf16)v1});
   }
 }
+
 // one wave per (sequence, 16-token group, head, 64-column block), the last fastest
 template <bool F16>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, KvTokens kt, KvTokens vt, int span, int waves) {

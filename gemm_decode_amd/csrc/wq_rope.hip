@@ -9,6 +9,9 @@
 // are the same for every head, so sine and cosine are paid once per share, and a head's 8
 // pairs are two 16-byte loads and stores (one 32-byte run when interleaved).  What lies
 // behind the turned elements is copied by further threads of the same kind.
+//
+// Memory bounds it: 8191 tokens of 40 heads of 128, three axes: 40 us, 4.2 TB/s (a copy reaches
+// 5.2); one token of 28 heads of 256: 4 us, a launch.
 #include "wq_internal.h"
 
 namespace wq {
@@ -112,7 +115,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int turn_chunks, 
 
 wq_status launch_rope(const RopeArgs& a, hipStream_t s) {
   const int turn_chunks = (a.half + 7) / 8, chunks = turn_chunks + (a.dim - 2 * a.half + 7) / 8;
-  // shares of the heads: enough threads for 16 waves per CU, at most one head per thread
+  // shares of the heads: enough threads for 16 waves per CU (twice and four times as many, so
+  // that sines are taken more often: 41 and 44 us for 40), at most one head per thread
   const int64_t base = a.tokens * chunks, want = (int64_t)256 * 16 * 64;
   int64_t shares = (want + base - 1) / base;
   if (shares > a.heads) shares = a.heads;
