@@ -250,6 +250,7 @@ __device__ __forceinline__ void store_out8(const AttnArgs& a, int64_t tok, int q
 template <int DB, int NB>
 __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, int s, int hk, int step0, int step1,
                                             int64_t slot) {
+#pragma clang fp contract(off)  // (a score's product rounds once: the largest minus the maximum is 0, however large)
   constexpr int RS = 132;  // floats of a row of the exchange buffer (128 + 4: no bank conflicts)
   __shared__ float ex[kWaves * 16 * RS];
   __shared__ float stat_m[kWaves][16 * NB], stat_l[kWaves][16 * NB];
@@ -398,11 +399,11 @@ __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Tile& t, in
           for (int o = 0; o < 4 * DB; ++o) O[nb][o] *= f;
           m[nb] = mx;
         }
-        const float ref = (m[nb] == kNegInf ? 0.f : m[nb]) - kWeightBits;
+        const float ref = m[nb] == kNegInf ? 0.f : m[nb];
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(sc[e] - ref);
+          p[e] = __builtin_amdgcn_exp2f((sc[e] - ref) + kWeightBits);
           l[nb] += p[e];
           if (p[e] > 0.f) p[e] *= vf[e >> 2];  // (a masked weight stays 0 beside a NaN page)
         }
@@ -634,6 +635,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
   constexpr int CH = KT * 4 * DB;            // 16-byte chunks of a tile's keys (or values)
   static_assert(CH <= TH, "a thread decodes one chunk of each");
   __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][KB], lds_v[2][KB];
+  __shared__ float bases[32 * kTileWaves];  // of the rows (see `based`)
   __shared__ int64_t win_at[2 * WIN * NG];
   __shared__ __attribute__((aligned(16))) uint8_t win_ek[2 * WIN * NG], win_ev[2 * WIN * NG];
 
@@ -716,10 +718,9 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
     last = live ? last_key(a, t, i) : -1;
     first = live ? first_key(a, t, i) : 0;
   }
-  // keys that some row, and that every row, of this wave sees
+  // keys that every row of this wave sees
   const bool any_row = wr0 < t.r1;
   const int i_lo = (any_row ? wr0 : t.r0) / a.group, i_hi = any_row ? (wr1 - 1) / a.group : i_lo;
-  const int32_t some_last = any_row ? last_key(a, t, i_hi) : -1, some_first = first_key(a, t, i_lo);
   const int32_t all_last = last_key(a, t, i_lo), all_first = first_key(a, t, i_hi);
 
   // ---- codes of a tile: memory -> registers -> fp16 operands in LDS
@@ -787,6 +788,12 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
   f32x16_t O[2 * DB], S[MT];
   u32x4_t P[NG];
   float m = kNegInf, l = 0.f;
+  // A weight's exponent is one fused product and difference, as far off as the maximum was rounded:
+  // less than the 2 bits between a weight and fp16's end while the maximum is below 2^20, which
+  // it is where c < 2^-10 (a product's size is below 2^30).  Elsewhere a row's scores are first
+  // taken relative to a base of that size (m is, too), by products that round as the maximum's
+  // did.
+  int based = 0;  // some row of the wave has a base
 #pragma unroll
   for (int o = 0; o < 2 * DB; ++o)
 #pragma unroll
@@ -797,7 +804,8 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
   // what the weights of tile j need, in the phase that has room for it
   float c = 0.f;
   int sink = 0;
-  int cold = 0;  // not 0: a mask, a scale to take out of O or a poisoned page
+  int cold = 0;  // not 0: a mask, a scale to take out of O, a poisoned page or a base
+  auto far = [&]() __attribute__((always_inline)) { return (int)(__builtin_amdgcn_ballot_w64(c >= 0x1p-10f) != 0); };
   auto prepare = [&](int j) {
     const int32_t key0 = c0 + j * KT;
     // (held above 0: a masked -infinity stays one)
@@ -806,19 +814,20 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
     sink = evo - evr;  // <= 0
     evo = evr;
     // (a byte of 255 is the only one whose complement is 0)
-    cold = (int)(key0 + KT - 1 > all_last) | (int)(key0 < all_first) | sink |
+    cold = (int)(key0 + KT - 1 > all_last) | (int)(key0 < all_first) | sink | based | far() |
            (int)((~ev_0 - 0x01010101u) & ev_0 & 0x80808080u);
     asm volatile("" : "+v"(c));
   };
   // Multiply (j): O += P V of tile j - 1 (not at j = 0), S = K Q of tile j, and stage (j).  The
   // operands are read AHEAD products before their use into a ring of registers (6 measured the
-  // same at 2 and 3 blocks; at 4 it no longer fits them: 398 us against 253 for 1024 tokens
-  // behind 7168); every step stays where it is written.
+  // same as 3 at up to 3 blocks; at 4 blocks 6, 3 and 2 for 1024 tokens behind 7168: 398, 311
+  // and 241 us, what no longer fits the registers being read from memory in the loop); every
+  // step stays where it is written.
   constexpr int PV = NG * 2 * DB, QK = MT * KS;  // products
   constexpr int PACE = PV + QK < STAGE + 3 ? 2 : 1;  // steps of staging per product
   static_assert((STAGE + 2) / PACE < PV + QK, "the staging fits between the products");
   auto multiply = [&](int j, auto with_values) {
-    constexpr int FIRST = decltype(with_values)::value ? 0 : PV, AHEAD = 3;
+    constexpr int FIRST = decltype(with_values)::value ? 0 : PV, AHEAD = DB == 4 ? 2 : 3;
     const uint8_t *kp = kd + (j & 1) * KB, *vp = vd + ((j + 1) & 1) * KB;
     auto operand = [&](int i) { return *(const u32x4_t*)(i < PV ? vp + i * 1024 : kp + (i - PV) * 1024); };
     u32x4_t ring[AHEAD];
@@ -876,6 +885,30 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
         for (int o = 0; o < 2 * DB; ++o)
 #pragma unroll
           for (int e = 0; e < 16; ++e) O[o][e] *= f;
+      }
+      if (based | far()) {
+#pragma clang fp contract(off)
+        // (an index that keeps no register between the tiles)
+        float* at = bases + 32 * wave + (__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, opaque(0))) & 31);
+        const float base = based ? *at : 0.f;
+        float mx = kNegInf;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            S[mt][e] = S[mt][e] * c - base;
+            mx = fmaxf(mx, S[mt][e]);
+          }
+        c = 1.f;
+        mx = max_over_halves(mx);
+        const float by = mx > m && __builtin_fabsf(mx) >= 0x1p20f ? mx : 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[mt][e] -= by;
+        m -= by;
+        *at = base + by;
+        if (__builtin_amdgcn_ballot_w64(by != 0.f) != 0) based = 1;
       }
     }
     float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
@@ -954,7 +987,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DB == 1 ? 4 : 2) void attn_tile_ke
   const int i = row / a.group, qh = hk * a.group + row - i * a.group;
   const int64_t at = (t.row + i) * q_heads + qh;
   if (h == 0) {
-    const float lse2 = lg == 0.f ? kNegInf : m + __builtin_log2f(lg) - kWeightBits;
+    const float lse2 = lg == 0.f ? kNegInf : (based ? bases[32 * wave + r] : 0.f) + (m + __builtin_log2f(lg) - kWeightBits);
     if (!direct) a.part_l[split * all_rows + at] = lse2;
     else if (a.lse) a.lse[at] = lse2 * 0.69314718055994530942f;
   }

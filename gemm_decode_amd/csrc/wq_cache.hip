@@ -120,7 +120,7 @@ __global__ __launch_bounds__(WPP > 4 ? 64 * WPP : 256) void kv_write_kernel(KvAr
   const int64_t end = (int64_t)q.start + q.n;
   const int first_page = q.start >> a.tshift;
   const int64_t p0 = (int64_t)(first_page + pi) << a.tshift;  // position of the page's slot 0
-  const bool touched = p0 < end;                              // (not when q.n == 0)
+  const bool touched = q.n > 0 && p0 < end;
   const int lo = (int)max((int64_t)q.start - p0, (int64_t)0);  // new slots lo .. hi - 1
   const int hi = touched ? (int)min(end - p0, (int64_t)T) : 0;
   int page = -1;

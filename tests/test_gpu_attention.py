@@ -237,6 +237,20 @@ def test_strided_keys_uniform_batches_and_bad_tables(wqlib):
                 assert np.array_equal(f64(g)[s], r, equal_nan=True)
 
 
+@pytest.mark.parametrize("most", [4, 40])
+def test_sequences_without_tokens_touch_no_page(wqlib, most):
+    """A sequence of no rows that stands inside a page, as in a padded batch, leaves that page alone."""
+    T, heads, dim = 16, 2, 64
+    rng = np.random.default_rng(20)
+    cache = wqlib.KVCache(4, T, heads, dim)
+    for t in (cache.k_codes, cache.v_codes, cache.k_exps, cache.v_exps):
+        t.fill_(0)
+    k = draw(rng, (3, heads, dim), "bf16")
+    wqlib.wq_kv_write(cache, wqlib.KVBatch(i32([[0, 0, 0], [1, 2, 3]]), i32([5, 1]), i32([0, 0, 3]), most), k, k)
+    for t, per in ((cache.k_codes, T * heads * dim), (cache.v_codes, T * heads * dim), (cache.k_exps, heads), (cache.v_exps, heads)):
+        assert (t[:per] == 0).all() and (t[2 * per:] == 0).all() and (t[per:2 * per] != 0).any()
+
+
 def test_lengths_beyond_the_bounds_are_cut(wqlib):
     """max_tokens, the table's width, the tensors' rows and negative starts bound every access."""
     T, heads, dim = 16, 1, 64
@@ -412,6 +426,42 @@ def test_attention_strides(wqlib, n):
 def test_attention_query_sizes(wqlib, qmul, n):
     """Zero, tiny and large queries: uniform weights, and nearly all weight on one key."""
     attention_case(wqlib, "bf16", 32, 4, 2, 64, [(n + 150, n)], qmul=qmul, seed=9)
+
+
+@pytest.mark.parametrize("ws", [True, None])
+@pytest.mark.parametrize("power", [16, 20, 22, 24, 25, 26, 28, 33, 45, 80, 110])
+@pytest.mark.parametrize("n", [1, 70])
+def test_attention_huge_scores(wqlib, n, power, ws):
+    """Scores far beyond 2^24, where a difference of scores says little: an output is a mean of values
+    still, and that of its key where one stands out by more than the arithmetic is off."""
+    rng = np.random.default_rng(power)
+    T, heads, dim, kv = 32, 2, 64, 1700
+    table, pages = tables(rng, [kv], T)
+    k, v, q = (draw(rng, (m, heads * (1 + (m == n)), dim), "bf16") for m in (kv, kv, n))
+    q *= 2.0 ** power
+    cache, ref = wqlib.KVCache(pages, T, heads, dim), OA.PagedCache(pages, T, heads, dim)
+    wqlib.wq_kv_write(cache, wqlib.KVBatch(i32(table), i32([0]), None, kv), k, v)
+    ref.write(table[0], 0, f64(k), f64(v))
+    batch = wqlib.KVBatch(i32(table), i32([kv - n]), None, n)
+    buf = wqlib.workspace(wqlib.wq_kv_attention_workspace_size(cache, batch, 2 * heads, n)) if ws else None
+    out, lse = torch.empty_like(q), torch.empty(n, 2 * heads, device=DEV)
+    wqlib.wq_kv_attention(cache, batch, q, out, 0.25, lse=lse, ws=buf)
+    o, K, V, Q = f64(out), *ref.read(table[0], 0, kv), f64(q)
+    assert np.isfinite(o).all() and torch.isfinite(lse).all()
+    told = 0
+    for i in range(n):
+        last = kv - n + i + 1
+        for h in range(2 * heads):
+            s = 0.25 * (K[:last, h // 2] @ Q[i, h])
+            off = (dim + 8) * 2.0 ** -24 * 0.25 * (np.abs(K[:last, h // 2]) @ np.abs(Q[i, h])).max() + 1
+            assert abs(float(lse[i, h]) - s.max()) <= 2 * off + np.log(last)
+            assert np.all(np.abs(o[i, h]) <= np.abs(V[:last, h // 2]).max(axis=0) * (1 + 2.0 ** -7))
+            top, second = np.sort(s)[::-1][:2]
+            if top - second > 2 * off + 40:   # (e^-40: nothing is left of the others)
+                told += 1
+                r = V[s.argmax(), h // 2]
+                assert np.all(np.abs(o[i, h] - r) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(r) + 2.0 ** -38 * np.abs(V).max())
+    assert told > 0
 
 
 def test_attention_negative_and_zero_scale(wqlib):
