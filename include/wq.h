@@ -508,8 +508,9 @@ wq_status wq_rope(int act, const void* x, int64_t x_token_stride, int64_t x_head
  * without a rounding of its own, the values are exact in bf16, and when a later token
  * enlarges a page's scale its older codes only drop low bits (q' = rint(q / 2^d)): however
  * often that happens the dropped parts add up to less than one step of the final scale,
- * where a scale of max / 127 would round again at every change.  A NaN or an infinity sets b = 255: the page's values of that head read
- * as NaN, and every query that sees one of its tokens gives NaN.
+ * where a scale of max / 127 would round again at every change.  A NaN or an infinity sets
+ * b = 255: the page's values of that head read as NaN, and every query that sees one of its
+ * tokens gives NaN.
  *
  * Memory: k_codes and v_codes hold wq_kv_cache_sizes' code bytes each (16-byte aligned),
  * k_exps and v_exps its exponent bytes ([pages][heads], any alignment).  None needs
@@ -539,8 +540,9 @@ typedef struct {
  * position p lies in pool page table[s * table_width + p / page_tokens].  table, starts and
  * offsets are on the device.  tokens: rows of the token tensors; max_tokens: the most rows
  * any sequence has (a longer one is cut there).  Offsets are clamped into [0, tokens];
- * negative starts count as 0; positions beyond the table are cut off; a page number outside the pool is not
- * written and reads as NaN.  seqs and tokens may be 0. */
+ * negative starts count as 0; positions beyond the table are cut off; a page number outside
+ * the pool is not written and reads as NaN.  A sequence without rows touches no page.  seqs
+ * and tokens may be 0. */
 typedef struct {
   int64_t seqs;
   int64_t tokens;
@@ -568,8 +570,9 @@ wq_status wq_kv_write(const wq_kv_cache* cache, const wq_kv_batch* batch, int ac
 
 /* Read the batch's positions back: k, v [tokens][heads][head_dim] in the given type (the
  * values q * 2^e, exact in bf16 and rounded once in fp16; a value beyond the type's largest
- * finite one becomes that one; NaN for pages of exponent 255).  Alignment as for wq_kv_write; rows outside every
- * sequence's range, and rows whose position lies beyond the table, are not written. */
+ * finite one becomes that one; NaN for pages of exponent 255).  Alignment as for
+ * wq_kv_write; rows outside every sequence's range, and rows whose position lies beyond the
+ * table, are not written. */
 wq_status wq_kv_read(const wq_kv_cache* cache, const wq_kv_batch* batch, int act, void* k,
                      int64_t k_token_stride, int64_t k_head_stride, void* v, int64_t v_token_stride,
                      int64_t v_head_stride, void* stream);
@@ -592,7 +595,8 @@ wq_status wq_kv_read(const wq_kv_cache* cache, const wq_kv_batch* batch, int act
  * max_kv: an upper bound of every kv (0: the table's); keys beyond it are cut off, and the
  * work is split by it.  Scores, statistics and sums are fp32; the softmax weights enter the
  * second product as fp16 (scaled so that 38 binades below the row's largest survive), the
- * codes as exact fp16 values.
+ * codes as exact fp16 values.  A query row that holds a NaN or an infinity, or a score beyond
+ * fp32's largest number, gives a row of NaN.
  *
  * ws: room for the partial results of a split over the keys; wq_kv_attention_workspace_size
  * gives what the best split takes, less (or NULL) only splits less.  Results are

@@ -372,6 +372,22 @@ def test_attention_split_and_unsplit_agree_with_the_definition(wqlib, kv, n):
         attention_case(wqlib, "bf16", 64, 4, 1, 128, [(kv, n), (n + 1, n), (700, min(n, 700))], ws=ws, seed=n)
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim,n", [(2, 1, 64, 40), (1, 1, 128, 70), (2, 1, 192, 40), (1, 1, 256, 70),
+                                                  (4, 1, 64, 2), (2, 1, 256, 1)])
+@pytest.mark.parametrize("ws", [True, None])
+def test_attention_long_contexts(wqlib, heads, kv_heads, dim, n, ws):
+    """More pages than a kernel holds at a time, in one run over the keys and split."""
+    attention_case(wqlib, "bf16", 16, heads, kv_heads, dim, [(20003, n)], ws=ws, seed=n)
+
+
+@pytest.mark.parametrize("wide", [0, 200])
+@pytest.mark.parametrize("seqs", [1024, 1025])
+def test_attention_many_sequences(wqlib, seqs, wide):
+    rng = np.random.default_rng(seqs)
+    lens = [(int(kv), min(int(kv), int(rng.integers(0, 3)))) for kv in rng.integers(0, 70, seqs)]
+    attention_case(wqlib, "bf16", 16, 2, 1, 64, lens, seed=3, wide=wide)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f16"])
 @pytest.mark.parametrize("heads,kv_heads,dim", HEADS)
 @pytest.mark.parametrize("n", [1, 5])
