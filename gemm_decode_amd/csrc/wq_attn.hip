@@ -1106,10 +1106,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int lanes) {
   if (a.lse && d == 0) a.lse[out_at] = sum == 0.f ? kNegInf : (mx + __builtin_log2f(sum)) * 0.69314718055994530942f;
 }
 
-// NB of the row kernel: the rows of the longest sequence, as far as the registers go
-int row_blocks(const AttnArgs& a) {
+// NB of the row kernel: the rows of the longest sequence, as far as the registers go; but every
+// tile of rows reads the codes (`bytes` of them at most) again, which costs less than the
+// larger tiles' latency while there are few.  Measured with NB 1, 2 and 4: 64 rows, 8 heads of
+// 128: 79 MB 28, 31, 46 us; 193 MB 43, 48, 56; 470 MB 192, 111, 114; 1 GB 430, 239, 224; 16
+// heads of 64: 195 MB 67, 60, 78; 474 MB 197, 125, 114; NB 1 and 2: 24 rows, 4 heads of 256:
+// 31 MB 18, 28; 78 MB 32, 32; 125 MB 36, 34; 1 GB 218, 124.
+int row_blocks(const AttnArgs& a, double bytes) {
   const int64_t rows = (int64_t)a.c.max_tokens * a.group;
-  const int top = a.c.blocks <= 2 ? 4 : 2;
+  const int top = bytes <= 1e8 ? 1 : bytes > 4e8 && a.c.blocks <= 2 ? 4 : 2;
   int nb = 1;
   while (nb < top && 16 * nb < rows) nb *= 2;
   return nb;
@@ -1143,15 +1148,16 @@ constexpr int kRowKernelRows = 64;
 int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
   const int64_t all = (int64_t)a->c.max_tokens * a->group;
   const bool tiled = all > kRowKernelRows;
-  a->tile_rows = tiled ? 32 * kTileWaves : 16 * row_blocks(*a);
+  auto seen_by = [&](int64_t rows) {  // keys that a tile of so many rows sees at most
+    return a->window > 0 ? std::min<int64_t>(a->cap, (int64_t)a->window + (rows - 1) / a->group + 2) : a->cap;
+  };
+  const double bytes = (double)a->c.seqs * a->c.heads * seen_by(all) * (128 * a->c.blocks);
+  a->tile_rows = tiled ? 32 * kTileWaves : 16 * row_blocks(*a, bytes);
   a->tiles = (int32_t)((all + a->tile_rows - 1) / a->tile_rows);
   a->shares = 0;
   a->chunk = INT32_MAX / 2;
   a->splits = 1;
-  // keys a row tile may see, rounded for its start at a multiple of 32
-  const int64_t q_tokens = (a->tile_rows - 1) / a->group + 2;
-  const int64_t seen = a->window > 0 ? std::min<int64_t>(a->cap, (int64_t)a->window + q_tokens) : a->cap;
-  const int64_t span = (seen + 2 * kStep - 1) / kStep * kStep;
+  const int64_t span = (seen_by(a->tile_rows) + 2 * kStep - 1) / kStep * kStep;  // (it starts at a multiple of 32)
   const int64_t items = (int64_t)a->c.seqs * a->c.heads * a->tiles;
   const int64_t most = (int64_t)(ws_bytes / ((64 * a->c.blocks + 1) * sizeof(float)));
   if (!tiled) {

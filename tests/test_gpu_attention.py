@@ -380,24 +380,25 @@ def test_attention_long_contexts(wqlib, heads, kv_heads, dim, n, ws):
     attention_case(wqlib, "bf16", 16, heads, kv_heads, dim, [(20003, n)], ws=ws, seed=n)
 
 
-@pytest.mark.parametrize("wide", [0, 200])
-@pytest.mark.parametrize("seqs", [1024, 1025])
-def test_attention_many_sequences(wqlib, seqs, wide):
+@pytest.mark.parametrize("wide", [0, 100, 210])
+@pytest.mark.parametrize("seqs,most", [(1024, 3), (1025, 3), (1025, 32)])
+def test_attention_many_sequences(wqlib, seqs, most, wide):
     rng = np.random.default_rng(seqs)
-    lens = [(int(kv), min(int(kv), int(rng.integers(0, 3)))) for kv in rng.integers(0, 70, seqs)]
+    lens = [(int(kv), min(int(kv), int(rng.integers(0, most)))) for kv in rng.integers(0, 70, seqs)]
     attention_case(wqlib, "bf16", 16, 2, 1, 64, lens, seed=3, wide=wide)
 
 
 @pytest.mark.parametrize("act", ["bf16", "f16"])
 @pytest.mark.parametrize("heads,kv_heads,dim", HEADS)
-@pytest.mark.parametrize("n", [1, 5])
-def test_attention_equal_shares(wqlib, act, heads, kv_heads, dim, n):
-    """Sequences that may be long: equal shares of all the work, whatever the lengths turn out to
-    be, none and one among them; and one long sequence among empty ones."""
+@pytest.mark.parametrize("n,wide", [(1, 600), (5, 600), (9, 3000), (30, 600), (64, 3000), (64, 30000)])
+def test_attention_equal_shares(wqlib, act, heads, kv_heads, dim, n, wide):
+    """Sequences that may be long (how long decides the rows of a tile): equal shares of all the
+    work, whatever the lengths turn out to be, none and one among them; and one long sequence among
+    empty ones."""
     n = min(n, 64 * kv_heads // heads)
     lens = [(0, 0), (n, n), (1, 0), (n + 1, n), (31 + n, 1), (32, 1), (33, 1), (700, n), (0, 0), (129, 1)]
-    attention_case(wqlib, act, 32, heads, kv_heads, dim, lens, wide=600, seed=dim + n)
-    attention_case(wqlib, act, 32, heads, kv_heads, dim, [(0, 0), (1500, n), (0, 0)], wide=600, seed=dim)
+    attention_case(wqlib, act, 32, heads, kv_heads, dim, lens, wide=wide, seed=dim + n)
+    attention_case(wqlib, act, 32, heads, kv_heads, dim, [(0, 0), (1500, n), (0, 0)], wide=wide, seed=dim)
 
 
 @pytest.mark.parametrize("window", [0, 2500])
