@@ -1138,20 +1138,27 @@ bool items_alone(int64_t items, int64_t span, int blocks, int64_t cus) {
 // 1024 tokens behind 7168: 303 us with 250, 253 with 1000 and 3000, 408 without a split)
 constexpr int64_t kTileCost = 3000;
 
-// More rows than this take the tile kernel: 64 rows, 32 sequences of 4000 keys, 8 heads of 128:
-// 100 us in the row kernel, 122 in the tile kernel; 80 rows: 178 and 121; one sequence: 30 and
-// 26, 31 and 27.
-constexpr int kRowKernelRows = 64;
+// Which kernel: up to 64 rows the row kernel; beyond, while there is little to do (workgroups of
+// 16 rows for at most six on a CU, codes read by all of them at most 600 MB), its short chain
+// counts for more than the tile kernel's economy.  Measured, row and tile kernel, 32 over 8 heads
+// of 128: 64 rows, 32 sequences of 4000 keys: 100, 122 us; 80 rows: 178, 121; a prompt of 200
+// tokens: 8, 17; of 500: 15, 28; three of 200 behind 1000 (369 MB): 32, 44; 16 sequences, 48
+// tokens behind 500 (1536 workgroups): 22, 27; three prompts of 333 (2016 workgroups): 23, 21; 16
+// times 96 behind 500 (3072 workgroups, 469 MB): 36, 30.
+bool few_rows(int64_t all, int64_t heads, double bytes, int64_t cus) {
+  const int64_t tiles = (all + 15) / 16;
+  return all <= 64 || (tiles <= 6 * cus && heads * tiles <= 6 * cus && bytes * tiles <= 6e8);
+}
 
 }  // namespace
 
 int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
   const int64_t all = (int64_t)a->c.max_tokens * a->group;
-  const bool tiled = all > kRowKernelRows;
   auto seen_by = [&](int64_t rows) {  // keys that a tile of so many rows sees at most
     return a->window > 0 ? std::min<int64_t>(a->cap, (int64_t)a->window + (rows - 1) / a->group + 2) : a->cap;
   };
   const double bytes = (double)a->c.seqs * a->c.heads * seen_by(all) * (128 * a->c.blocks);
+  const bool tiled = !few_rows(all, std::min<int64_t>((int64_t)a->c.seqs * a->c.heads, INT32_MAX), bytes, device_cus());
   a->tile_rows = tiled ? 32 * kTileWaves : 16 * row_blocks(*a, bytes);
   a->tiles = (int32_t)((all + a->tile_rows - 1) / a->tile_rows);
   a->shares = 0;
@@ -1196,7 +1203,7 @@ int64_t plan_attention(AttnArgs* a, size_t ws_bytes) {
 wq_status launch_attention(const AttnArgs& a, hipStream_t s) {
   const __int128 items = (__int128)a.c.seqs * a.c.heads * a.tiles * a.splits;
   if (items > INT32_MAX - 8 * (__int128)a.tiles) return fail(WQ_ERR_UNSUPPORTED, "wq_kv_attention: too many rows for one call");
-  if ((int64_t)a.c.max_tokens * a.group > kRowKernelRows) {
+  if (a.tile_rows == 32 * kTileWaves) {
     const uint32_t pairs = (uint32_t)(items / a.tiles);
     // 12 pairs of 4000 rows: 307 us spread, 381 not; 4 pairs of 28672: 289 and 401; 192 pairs of
     // 2581 rows: 363 and 335; 8 pairs: 157 and 160

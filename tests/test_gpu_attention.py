@@ -55,7 +55,22 @@ def tables(rng, lens, T, spare=3):
     t = np.full((len(lens), max(need) + 1), -1, dtype=np.int32)
     for b, m in enumerate(need):
         t[b, :m], order = order[:m], order[m:]
+    if ROOM > t.shape[1]:
+        t = np.pad(t, ((0, 0), (0, ROOM - t.shape[1])), constant_values=-1)
     return t, sum(need) + spare
+
+
+ROOM = 0  # the least width of the page tables
+
+
+@pytest.fixture(params=[0, 60000], ids=["tight", "roomy"])
+def room(request):
+    """Tables as wide as the sequences need, and tables with room for many times more: what a sequence
+    may hold decides the kernel, the rows of a tile and the split."""
+    global ROOM
+    ROOM = request.param
+    yield
+    ROOM = 0
 
 
 # ------------------------------------------------------------------------------- rope
@@ -306,7 +321,7 @@ def attention_case(wqlib, act, T, heads, kv_heads, dim, lens, causal=True, windo
     batch = wqlib.KVBatch(i32(table), i32([kv - n for kv, n in lens]), i32(qo), max(1, max(ns)))
     buf = wqlib.workspace(wqlib.wq_kv_attention_workspace_size(cache, batch, heads, int(qo[-1]))) if ws is True else ws
     wqlib.wq_kv_attention(cache, batch, q, out, scale, causal=causal, window=window, lse=sums, ws=buf,
-                          kv_lens=None if kv_lens is None else i32(kv_lens), max_kv=(0 if wide else max(kvs)) if max_kv is None else max_kv)
+                          kv_lens=None if kv_lens is None else i32(kv_lens), max_kv=(0 if wide or ROOM else max(kvs)) if max_kv is None else max_kv)
     o = f64(out)
     for b, (kv, n) in enumerate(lens):
         K, V = ref.read(table[b], 0, kv)
@@ -326,6 +341,7 @@ def attention_case(wqlib, act, T, heads, kv_heads, dim, lens, causal=True, windo
 HEADS = [(4, 4, 64), (8, 2, 128), (24, 4, 256), (7, 1, 80), (12, 1, 192), (32, 2, 8)]
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("act", ["bf16", "f16"])
 @pytest.mark.parametrize("heads,kv_heads,dim", HEADS)
 @pytest.mark.parametrize("T", [16, 64])
@@ -334,30 +350,35 @@ def test_attention_single_tokens(wqlib, act, heads, kv_heads, dim, T):
     attention_case(wqlib, act, T, heads, kv_heads, dim, lens, seed=dim + T)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("act", ["bf16", "f16"])
 @pytest.mark.parametrize("heads,kv_heads,dim", HEADS)
 def test_attention_prompts(wqlib, act, heads, kv_heads, dim):
     attention_case(wqlib, act, 32, heads, kv_heads, dim, [(1, 1), (70, 70), (0, 0), (201, 90), (33, 2), (64, 64)], seed=dim)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("T", [16, 32, 64, 128])
 @pytest.mark.parametrize("n", [1, 3, 8, 65, 150])
 def test_attention_row_counts_and_pages(wqlib, T, n):
     attention_case(wqlib, "bf16", T, 6, 2, 128, [(n, n), (n + 100, n), (n + 1, n)], seed=n)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 10 ** 6])
 @pytest.mark.parametrize("n", [1, 5, 130])
 def test_attention_windows(wqlib, window, n):
     attention_case(wqlib, "bf16", 32, 4, 2, 64, [(n, n), (n + 77, n), (n + 300, n)], window=window, seed=window)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [1, 4, 70])
 def test_attention_not_causal(wqlib, n):
     attention_case(wqlib, "f16", 16, 4, 2, 64, [(200, n), (1, n), (0, n), (31, n)], causal=False,
                    kv_lens=[200, 1, 0, 31], seed=n)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [3, 40, 200])
 def test_attention_rows_that_see_nothing(wqlib, n):
     """More queries than keys: the first rows stand before the cache's first token."""
@@ -366,12 +387,14 @@ def test_attention_rows_that_see_nothing(wqlib, n):
     assert (out[: n - 2] == 0).all() and (out[n:2 * n] == 0).all()
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("kv,n", [(3000, 1), (3001, 7), (2999, 80), (4100, 300)])
 def test_attention_split_and_unsplit_agree_with_the_definition(wqlib, kv, n):
     for ws in (True, None, torch.empty(1 << 18, dtype=torch.uint8, device=DEV)):
         attention_case(wqlib, "bf16", 64, 4, 1, 128, [(kv, n), (n + 1, n), (700, min(n, 700))], ws=ws, seed=n)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("heads,kv_heads,dim,n", [(2, 1, 64, 40), (1, 1, 128, 70), (2, 1, 192, 40), (1, 1, 256, 70),
                                                   (4, 1, 64, 2), (2, 1, 256, 1)])
 @pytest.mark.parametrize("ws", [True, None])
@@ -433,11 +456,13 @@ def test_attention_equal_shares_keep_a_poisoned_page_in_its_sequence(wqlib):
     assert torch.equal(outs[0], outs[1])
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [1, 90])
 def test_attention_strides(wqlib, n):
     attention_case(wqlib, "bf16", 32, 6, 3, 80, [(n + 40, n), (n, n)], strided=True, lse=False)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("qmul", [0.0, 2.0 ** -100, 2.0 ** -20, 64.0])
 @pytest.mark.parametrize("n", [1, 70])
 def test_attention_query_sizes(wqlib, qmul, n):
@@ -445,6 +470,7 @@ def test_attention_query_sizes(wqlib, qmul, n):
     attention_case(wqlib, "bf16", 32, 4, 2, 64, [(n + 150, n)], qmul=qmul, seed=9)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("ws", [True, None])
 @pytest.mark.parametrize("power", [16, 20, 22, 24, 25, 26, 28, 33, 45, 80, 110])
 @pytest.mark.parametrize("n", [1, 70])
@@ -481,11 +507,13 @@ def test_attention_huge_scores(wqlib, n, power, ws):
     assert told > 0
 
 
+@pytest.mark.usefixtures("room")
 def test_attention_negative_and_zero_scale(wqlib):
     for scale in (-0.2, 0.0):
         attention_case(wqlib, "bf16", 32, 4, 2, 64, [(90, 3)], scale=scale)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [1, 100])
 def test_attention_values_of_different_scales(wqlib, n):
     """Pages 2^60 apart in size, growing, falling: every page's weight keeps its own scale."""
@@ -508,6 +536,7 @@ def test_attention_values_of_different_scales(wqlib, n):
         assert np.all(np.abs(f64(out) - r) <= tol)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [1, 40, 140])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("side", ["k", "v"])
@@ -538,6 +567,7 @@ def test_attention_poisoned_pages_reach_only_rows_that_see_them(wqlib, n, bad, s
         assert np.allclose(o[i], r[i], atol=2e-2, rtol=2e-2)
 
 
+@pytest.mark.usefixtures("room")
 def test_attention_bad_queries_stay_in_their_rows(wqlib):
     rng = np.random.default_rng(13)
     T, heads, dim, kv, n = 32, 2, 64, 100, 20
@@ -603,6 +633,7 @@ def test_attention_in_a_pool_beyond_4_gib(wqlib):
     assert np.all(np.abs(f64(out) - r) <= 2.0 ** -8 * np.abs(r) + (2.0 ** -11 + 2 * e) * mass + least_weight(rv, heads))
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [1, 100])
 def test_attention_same_bits_every_time_and_in_a_graph(wqlib, n):
     rng = np.random.default_rng(16)
@@ -649,6 +680,7 @@ def test_attention_same_bits_every_time_and_in_a_graph(wqlib, n):
         assert torch.equal(got, outs[0]), i
 
 
+@pytest.mark.usefixtures("room")
 def test_attention_on_another_stream(wqlib):
     rng = np.random.default_rng(17)
     T, heads, dim, kv = 32, 2, 64, 300
