@@ -538,7 +538,7 @@ __global__ __launch_bounds__(64 * kWaves, DB * NB <= 2 ? 3 : DB * NB <= 4 ? 2 : 
 }
 
 // ----------------------------------------------------------------- the tile kernel
-// Many rows per key/value head (prompts): a workgroup of 8 waves takes 256 rows, 32 to a
+// Many rows per key/value head (long prompts): a workgroup of 8 waves takes 256 rows, 32 to a
 // wave, and walks the keys in tiles of KT.  The waves decode a tile's codes together into
 // fp16 operands in LDS, once for all rows, the codes of the next tile in flight in
 // registers; every wave multiplies its own rows by the whole tile on
@@ -546,9 +546,9 @@ __global__ __launch_bounds__(64 * kWaves, DB * NB <= 2 ? 3 : DB * NB <= 4 ? 2 : 
 // us against 560) and 32 beyond, where a tile of 64 has more chunks than there are threads and
 // the scores no registers.
 //
-// Measured: 8192-token prompt, 32 over 8 heads of 128: 544 us, 1010 TFLOP/s (the products alone
-// 455 at a library product's rate); 1024 tokens behind 7168, 24 over 4 heads of 256: 246 us, 784
-// TFLOP/s; 12 prompts of up to 2581, 16 heads of 64: 184 us, 500 TFLOP/s.  The vector units
+// Measured: 8192-token prompt, 32 over 8 heads of 128: 545 to 573 us, 960 to 1010 TFLOP/s (the
+// products alone 455 at a library product's rate); 1024 tokens behind 7168, 24 over 4 heads of
+// 256: 242 us, 800 TFLOP/s; 12 prompts of up to 2581, 16 heads of 64: 184 us, 500 TFLOP/s.  The vector units
 // bound it at 64 columns (a weight costs the same, its products half of those at 128), products
 // and weights about alike at 128, operands and the joining of splits at 256.
 //
@@ -1144,7 +1144,7 @@ constexpr int64_t kTileCost = 3000;
 // of 128: 64 rows, 32 sequences of 4000 keys: 100, 122 us; 80 rows: 178, 121; a prompt of 200
 // tokens: 8, 17; of 500: 15, 28; three of 200 behind 1000 (369 MB): 32, 44; 16 sequences, 48
 // tokens behind 500 (1536 workgroups): 22, 27; three prompts of 333 (2016 workgroups): 23, 21; 16
-// times 96 behind 500 (3072 workgroups, 469 MB): 36, 30.
+// times 96 behind 500 (twice 1536): 36, 30.
 bool few_rows(int64_t all, int64_t heads, double bytes, int64_t cus) {
   const int64_t tiles = (all + 15) / 16;
   return all <= 64 || (tiles <= 6 * cus && heads * tiles <= 6 * cus && bytes * tiles <= 6e8);
